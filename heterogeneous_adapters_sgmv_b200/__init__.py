@@ -37,14 +37,26 @@ LORA_SIGMA_NONE = 0
 LORA_SIGMA_FULL = 1
 LORA_SIGMA_DIAG = 2
 LORA_MAX_MERGE = 8
-LORA_KERNEL_KINDS = 7
+LORA_KERNEL_KINDS = 11
+LORA_ACT_NONE = 0
+LORA_ACT_RELU = 1
+LORA_ACT_GELU = 2
+LORA_ACT_GELU_TANH = 3
+LORA_ACT_SILU = 4
+LORA_NORM_RMS = 1
+LORA_NORM_LAYER = 2
+LORA_GATE_NONE = 0
+LORA_GATE_ADAPTER = 1
+LORA_GATE_TOKEN = 2
+LORA_MAX_NORM_WIDTH = 16384
 
 EXPORTS = (
     "lora_table_create", "lora_table_destroy", "lora_table_info", "lora_workspace_bytes",
     "lora_build_segments", "lora_shrink", "lora_expand", "lora_sgmv", "lora_bgmv",
     "lora_get_status", "lora_status_string", "lora_set_option", "lora_get_option",
     "lora_sgmv_noalloc", "lora_sgmv_grouped", "lora_table_set_sigma", "lora_bgmv_merged",
-    "lora_sgmv_base", "lora_kernel_name", "lora_kernel_launches",
+    "lora_sgmv_base", "lora_kernel_name", "lora_kernel_launches", "lora_sgmv_layer", "lora_bgmv_layer",
+    "lora_norm_before", "lora_norm_after",
 )
 
 
@@ -65,6 +77,47 @@ class lora_segments(ctypes.Structure):
         ("T", ctypes.c_int32),
         ("max_segs", ctypes.c_int32),
         ("max_seg_len", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class lora_epilogue(ctypes.Structure):
+    """Mirror of ``struct lora_epilogue`` (what follows a layer's product)."""
+
+    _fields_ = [
+        ("bias", ctypes.c_void_p),
+        ("mul", ctypes.c_void_p),
+        ("residual", ctypes.c_void_p),
+        ("ldmul", ctypes.c_int64),
+        ("ldres", ctypes.c_int64),
+        ("act", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class lora_norm(ctypes.Structure):
+    """Mirror of ``struct lora_norm`` (one normalisation and its weights)."""
+
+    _fields_ = [
+        ("gain", ctypes.c_void_p),
+        ("shift", ctypes.c_void_p),
+        ("ld", ctypes.c_int64),
+        ("eps", ctypes.c_float),
+        ("kind", ctypes.c_int32),
+    ]
+
+
+class lora_residual(ctypes.Structure):
+    """Mirror of ``struct lora_residual`` (how a block's output joins the residual stream)."""
+
+    _fields_ = [
+        ("residual", ctypes.c_void_p),
+        ("gate", ctypes.c_void_p),
+        ("ldres", ctypes.c_int64),
+        ("ldgate", ctypes.c_int64),
+        ("res_scale", ctypes.c_float),
+        ("branch_scale", ctypes.c_float),
+        ("gate_kind", ctypes.c_int32),
         ("reserved", ctypes.c_int32),
     ]
 
@@ -96,6 +149,13 @@ def _load():
         "lora_sgmv_base": ([P, ctypes.POINTER(lora_segments), P, I64, P, I64, P, I64, I32, I32, P, SZ, P],
                            ctypes.c_int),
         "lora_sgmv_grouped": ([P, I32, ctypes.POINTER(lora_segments), P, P, P, P, P, P, SZ, P], ctypes.c_int),
+        "lora_sgmv_layer": ([P, ctypes.POINTER(lora_segments), P, I64, P, I64, ctypes.POINTER(lora_epilogue), P, I64,
+                             I32, P, SZ, P], ctypes.c_int),
+        "lora_bgmv_layer": ([P, P, I32, P, I64, P, I64, ctypes.POINTER(lora_epilogue), P, I64, I32, P, SZ, P],
+                            ctypes.c_int),
+        "lora_norm_before": ([P, P, I32, I32, P, I64, ctypes.POINTER(lora_norm), P, I64, P], ctypes.c_int),
+        "lora_norm_after": ([P, P, I32, I32, P, I64, ctypes.POINTER(lora_norm), ctypes.POINTER(lora_residual), P, I64,
+                             ctypes.POINTER(lora_norm), P, I64, P], ctypes.c_int),
         "lora_get_status": ([P, ctypes.POINTER(ctypes.c_uint32), I32, P], ctypes.c_int),
         "lora_status_string": ([ctypes.c_int], ctypes.c_char_p),
         "lora_set_option": ([ctypes.c_char_p, I64], ctypes.c_int),
@@ -237,6 +297,56 @@ def lora_bgmv(table: int, ids, T: int, x, ldx: int, y, ldy: int, y_offset: int, 
               stream=None) -> None:
     _check(_load().lora_bgmv(table, _ptr(ids), T, _ptr(x), ldx, _ptr(y), ldy, y_offset, _ptr(ws), ws_bytes,
                              _stream(stream)), "lora_bgmv")
+
+
+def make_epilogue(bias=None, act: int = LORA_ACT_NONE, mul=None, ldmul: int = 0, residual=None,
+                  ldres: int = 0) -> lora_epilogue:
+    """y = act(z + bias) * mul + residual; the caller keeps the tensors alive."""
+    return lora_epilogue(_ptr(bias), _ptr(mul), _ptr(residual), ldmul, ldres, act, 0)
+
+
+def make_norm(kind: int, eps: float, gain=None, shift=None, ld: int = 0) -> lora_norm:
+    """One normalisation; with ld > 0 gain and shift hold 1 + n rows, row 0 the base model's and
+    row 1 + i adapter i's.  The caller keeps the tensors alive."""
+    return lora_norm(_ptr(gain), _ptr(shift), ld, eps, kind)
+
+
+def make_residual(residual=None, ldres: int = 0, gate=None, ldgate: int = 0, gate_kind: int = LORA_GATE_NONE,
+                  res_scale: float = 1.0, branch_scale: float = 1.0) -> lora_residual:
+    """r = res_scale * residual + branch_scale * gate * u; the caller keeps the tensors alive."""
+    return lora_residual(_ptr(residual), _ptr(gate), ldres, ldgate, res_scale, branch_scale, gate_kind, 0)
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
+
+
+def lora_sgmv_layer(table: int, seg: lora_segments, x, ldx: int, W, ldw: int, epilogue: Optional[lora_epilogue], y,
+                    ldy: int, y_offset: int, ws=None, ws_bytes: int = 0, stream=None) -> None:
+    """A whole layer over contiguous segments: x W^T + s_i B_i A_i x, then the epilogue (None: none)."""
+    _check(_load().lora_sgmv_layer(table, ctypes.byref(seg), _ptr(x), ldx, _ptr(W), ldw, _ref(epilogue), _ptr(y), ldy,
+                                   y_offset, _ptr(ws), ws_bytes, _stream(stream)), "lora_sgmv_layer")
+
+
+def lora_bgmv_layer(table: int, ids, T: int, x, ldx: int, W, ldw: int, epilogue: Optional[lora_epilogue], y, ldy: int,
+                    y_offset: int, ws=None, ws_bytes: int = 0, stream=None) -> None:
+    """A whole layer driven by per-token ids (None: no token has an adapter)."""
+    _check(_load().lora_bgmv_layer(table, _ptr(ids), T, _ptr(x), ldx, _ptr(W), ldw, _ref(epilogue), _ptr(y), ldy,
+                                   y_offset, _ptr(ws), ws_bytes, _stream(stream)), "lora_bgmv_layer")
+
+
+def lora_norm_before(table: int, ids, T: int, d: int, x, ldx: int, norm: lora_norm, h, ldh: int, stream=None) -> None:
+    """The norm before a block, each token with its adapter's gains: h = N(x)."""
+    _check(_load().lora_norm_before(table, _ptr(ids), T, d, _ptr(x), ldx, _ref(norm), _ptr(h), ldh, _stream(stream)),
+           "lora_norm_before")
+
+
+def lora_norm_after(table: int, ids, T: int, d: int, z, ldz: int, norm: Optional[lora_norm], residual: lora_residual,
+                    r, ldr: int, next_norm: Optional[lora_norm] = None, h=None, ldh: int = 0, stream=None) -> None:
+    """The norm after a block, gate and residual, and the next block's norm, in one pass:
+    r = res_scale * residual + branch_scale * gate * N(z); h = N_next(r)."""
+    _check(_load().lora_norm_after(table, _ptr(ids), T, d, _ptr(z), ldz, _ref(norm), _ref(residual), _ptr(r), ldr,
+                                   _ref(next_norm), _ptr(h), ldh, _stream(stream)), "lora_norm_after")
 
 
 def lora_get_status(table: int, reset: bool = True, stream=None):

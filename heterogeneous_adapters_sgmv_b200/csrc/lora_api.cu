@@ -24,7 +24,8 @@ static int64_t env_or(const char *name, int64_t dflt)
 static std::atomic<int64_t> g_launches[kKernKinds];
 static const char *const kKernelNames[kKernKinds] = {
     "lora_decode_kernel", "count_segments_kernel", "build_segments_kernel", "prefill_shrink_kernel",
-    "prefill_expand_kernel", "base_gemm_kernel", "merge_finish_kernel",
+    "prefill_expand_kernel", "base_gemm_kernel", "merge_finish_kernel", "layer_shrink_kernel", "layer_stream_kernel",
+    "layer_gemm_kernel", "block_norm_kernel",
 };
 
 void note_launch(KernelKind k) { g_launches[k].fetch_add(1, std::memory_order_relaxed); }
@@ -173,6 +174,88 @@ void set_segments(DecodeParams &p, const lora_segments *seg)
     p.num_segs = seg->num_segs;
     p.max_segs = seg->max_segs;
     p.T = seg->T;
+}
+
+// The layer and norm calls run on the table's device, which must be the current one.
+int check_device(const lora_table *t)
+{
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) return LORA_ERR_CUDA;
+    return dev == t->device ? LORA_OK : LORA_ERR_INVALID_ARG;
+}
+
+// A row-major [rows, cols] operand of one element size, for the checks of what may overlap.
+struct Plane {
+    const void *p;
+    int64_t ld, cols;
+};
+
+// Whether writing plane a while plane b is read (or written) elsewhere could touch b.  Planes of
+// one row stride are compared by column interval, modulo the row, so that slices of one fused
+// buffer pass; others by the bytes they span.
+bool planes_overlap(const Plane &a, const Plane &b, int64_t rows, int e)
+{
+    if (!a.p || !b.p || rows <= 0) return false;
+    const int64_t a0 = (int64_t)reinterpret_cast<uintptr_t>(a.p), b0 = (int64_t)reinterpret_cast<uintptr_t>(b.p);
+    const int64_t a1 = a0 + ((rows - 1) * a.ld + a.cols) * e, b1 = b0 + ((rows - 1) * b.ld + b.cols) * e;
+    if (a0 >= b1 || b0 >= a1) return false;
+    if (a.ld != b.ld) return true;
+    const int64_t row = a.ld * e;
+    const int64_t off = ((b0 - a0) % row + row) % row;   // where b's first column falls in a's row
+    return off < a.cols * e || off + b.cols * e > row;
+}
+
+// The same, but an operand at a's own address and stride is allowed: each element is read by the
+// thread that writes it, before it does.
+bool planes_clash(const Plane &a, const Plane &b, int64_t rows, int e)
+{
+    return !(a.p == b.p && a.ld == b.ld) && planes_overlap(a, b, rows, e);
+}
+
+int check_epilogue(const lora_epilogue *e, const lora_table *t, int32_t T, const void *x, int64_t ldx, const void *y,
+                   int64_t ldy, int32_t y_off)
+{
+    const int sz = esz(t->dtype), c = epc(t->dtype);
+    const Plane out = {static_cast<const uint8_t *>(y) + (int64_t)y_off * sz, ldy, t->o};
+    if (planes_overlap(out, {x, ldx, t->h}, T, sz)) return LORA_ERR_INVALID_ARG;
+    if (!e) return LORA_OK;
+    if (e->act < LORA_ACT_NONE || e->act > LORA_ACT_SILU) return LORA_ERR_INVALID_ARG;
+    if ((e->mul && e->ldmul < t->o) || (e->residual && e->ldres < t->o)) return LORA_ERR_INVALID_ARG;
+    if (!al16(e->bias) || !al16(e->mul) || !al16(e->residual)) return LORA_ERR_UNSUPPORTED;
+    if ((e->mul && e->ldmul % c) || (e->residual && e->ldres % c)) return LORA_ERR_UNSUPPORTED;
+    if (planes_clash(out, {e->mul, e->ldmul, t->o}, T, sz) || planes_clash(out, {e->residual, e->ldres, t->o}, T, sz))
+        return LORA_ERR_INVALID_ARG;
+    return LORA_OK;
+}
+
+// A weight that a token takes by its adapter: one row (ld 0) or 1 + n rows.
+int check_rows(const void *w, int64_t ld, int32_t d, int dtype)
+{
+    if (!w) return LORA_OK;
+    if (ld != 0 && ld < d) return LORA_ERR_INVALID_ARG;
+    return (al16(w) && ld % epc(dtype) == 0) ? LORA_OK : LORA_ERR_UNSUPPORTED;
+}
+
+int check_norm(const lora_norm *nm, int32_t d, int dtype)
+{
+    if (nm->kind != LORA_NORM_RMS && nm->kind != LORA_NORM_LAYER) return LORA_ERR_INVALID_ARG;
+    if (!(nm->eps >= 0.f) || nm->eps > 3.4e38f) return LORA_ERR_INVALID_ARG;
+    const int rc = check_rows(nm->gain, nm->ld, d, dtype);
+    return rc ? rc : check_rows(nm->shift, nm->ld, d, dtype);
+}
+
+int check_plane(const void *p, int64_t ld, int32_t d, int dtype)
+{
+    if (!p || ld < d) return LORA_ERR_INVALID_ARG;
+    return (al16(p) && ld % epc(dtype) == 0) ? LORA_OK : LORA_ERR_UNSUPPORTED;
+}
+
+int check_norm_call(const lora_table *t, int32_t T, int32_t d)
+{
+    const int rc = check_table(t);
+    if (rc) return rc;
+    if (T < 0 || d < 1) return LORA_ERR_INVALID_ARG;
+    return (d % epc(t->dtype) || d > LORA_MAX_NORM_WIDTH) ? LORA_ERR_UNSUPPORTED : LORA_OK;
 }
 
 }  // namespace
@@ -618,6 +701,130 @@ int lora_bgmv_merged(const lora_table *t, const int32_t *d_ids, const float *d_w
     }
     if (yacc) return launch_merge_finish(y, ldy, y_off, yacc, t->o, T, t->o, t->dtype, s);
     return LORA_OK;
+}
+
+int lora_sgmv_layer(const lora_table *t, const lora_segments *seg, const void *x, int64_t ldx, const void *W,
+                    int64_t ldw, const lora_epilogue *epi, void *y, int64_t ldy, int32_t y_off, void *ws,
+                    size_t ws_bytes, void *stream)
+{
+    int rc = check_table(t);
+    if (rc) return rc;
+    if ((rc = check_segments(seg))) return rc;
+    if ((rc = check_io(t, x, ldx, y, ldy, y_off, true, true))) return rc;
+    if (!W || ldw < t->h) return LORA_ERR_INVALID_ARG;
+    if (!al16(W) || ldw % 8) return LORA_ERR_UNSUPPORTED;
+    if (!prefill_supported(t) || seg->perm != nullptr) return LORA_ERR_UNSUPPORTED;
+    if ((rc = check_epilogue(epi, t, seg->T, x, ldx, y, ldy, y_off))) return rc;
+    if (seg->T == 0) return LORA_OK;
+    const WsLayout w = ws_layout(t, seg->T);
+    if (!ws || ws_bytes < w.total) return LORA_ERR_WORKSPACE;
+    if (!al16(ws)) return LORA_ERR_UNSUPPORTED;
+    if ((rc = check_device(t))) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    void *v = static_cast<uint8_t *>(ws) + w.v;
+    const bool shrink = seg->max_segs > 0;
+    if (shrink && (rc = launch_prefill_shrink(t, seg, x, ldx, v, true, s)) != LORA_OK) return rc;
+    const lora_epilogue none = {};
+    return launch_layer_gemm(t, seg, x, ldx, W, ldw, epi ? epi : &none, y, ldy, y_off, v, shrink, s);
+}
+
+int lora_bgmv_layer(const lora_table *t, const int32_t *d_ids, int32_t T, const void *x, int64_t ldx, const void *W,
+                    int64_t ldw, const lora_epilogue *epi, void *y, int64_t ldy, int32_t y_off, void *ws,
+                    size_t ws_bytes, void *stream)
+{
+    int rc = check_table(t);
+    if (rc) return rc;
+    if (T < 0) return LORA_ERR_INVALID_ARG;
+    if ((rc = check_io(t, x, ldx, y, ldy, y_off, true, true))) return rc;
+    if (!W || ldw < t->h) return LORA_ERR_INVALID_ARG;
+    if (!al16(W) || ldw % 8) return LORA_ERR_UNSUPPORTED;
+    if (t->dtype != LORA_BF16 || t->sigma_kind != LORA_SIGMA_NONE) return LORA_ERR_UNSUPPORTED;
+    if ((rc = check_epilogue(epi, t, T, x, ldx, y, ldy, y_off))) return rc;
+    if (T == 0) return LORA_OK;
+    const WsLayout w = ws_layout(t, T);
+    if (d_ids) {
+        if (!ws || ws_bytes < w.total) return LORA_ERR_WORKSPACE;
+        if (!al16(ws)) return LORA_ERR_UNSUPPORTED;
+    }
+    if ((rc = check_device(t))) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    float *v = nullptr;
+    if (d_ids) {
+        v = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.v);
+        if ((rc = launch_layer_shrink(t, d_ids, T, x, ldx, v, ldv_of(t), s)) != LORA_OK) return rc;
+    }
+    const lora_epilogue none = {};
+    return launch_layer_stream(t, d_ids, T, x, ldx, W, ldw, epi ? epi : &none, y, ldy, y_off, v, ldv_of(t), s);
+}
+
+int lora_norm_before(const lora_table *t, const int32_t *d_ids, int32_t T, int32_t d, const void *x, int64_t ldx,
+                     const lora_norm *norm, void *h, int64_t ldh, void *stream)
+{
+    int rc = check_norm_call(t, T, d);
+    if (rc) return rc;
+    if (!norm) return LORA_ERR_INVALID_ARG;
+    if ((rc = check_norm(norm, d, t->dtype))) return rc;
+    if ((rc = check_plane(x, ldx, d, t->dtype)) || (rc = check_plane(h, ldh, d, t->dtype))) return rc;
+    if (planes_clash({h, ldh, d}, {x, ldx, d}, T, esz(t->dtype))) return LORA_ERR_INVALID_ARG;
+    if (T == 0) return LORA_OK;
+    if ((rc = check_device(t))) return rc;
+    NormParams p = {};
+    p.ids = d_ids;
+    p.T = T;
+    p.d = d;
+    p.n = t->n;
+    p.x = x;
+    p.ldx = ldx;
+    p.norm = *norm;
+    p.h = h;
+    p.ldh = ldh;
+    p.status = t->d_status;
+    return launch_block_norm(p, false, t->dtype, static_cast<cudaStream_t>(stream));
+}
+
+int lora_norm_after(const lora_table *t, const int32_t *d_ids, int32_t T, int32_t d, const void *z, int64_t ldz,
+                    const lora_norm *norm, const lora_residual *res, void *r, int64_t ldr, const lora_norm *next,
+                    void *h, int64_t ldh, void *stream)
+{
+    int rc = check_norm_call(t, T, d);
+    if (rc) return rc;
+    const int dt = t->dtype, e = esz(dt);
+    if (!res || (!r && !h) || !next != !h) return LORA_ERR_INVALID_ARG;
+    if (norm && (rc = check_norm(norm, d, dt))) return rc;
+    if (next && (rc = check_norm(next, d, dt))) return rc;
+    if ((rc = check_plane(z, ldz, d, dt))) return rc;
+    if (res->residual && (rc = check_plane(res->residual, res->ldres, d, dt))) return rc;
+    if (r && (rc = check_plane(r, ldr, d, dt))) return rc;
+    if (h && (rc = check_plane(h, ldh, d, dt))) return rc;
+    if (res->gate_kind < LORA_GATE_NONE || res->gate_kind > LORA_GATE_TOKEN) return LORA_ERR_INVALID_ARG;
+    if (res->gate_kind != LORA_GATE_NONE && !res->gate) return LORA_ERR_INVALID_ARG;
+    if (res->gate_kind == LORA_GATE_ADAPTER && (rc = check_rows(res->gate, res->ldgate, d, dt))) return rc;
+    if (res->gate_kind == LORA_GATE_TOKEN && (rc = check_plane(res->gate, res->ldgate, d, dt))) return rc;
+    const Plane pr = {r, ldr, d}, ph = {h, ldh, d};
+    const Plane in[3] = {{z, ldz, d},
+                         {res->residual, res->ldres, d},
+                         {res->gate_kind == LORA_GATE_TOKEN ? res->gate : nullptr, res->ldgate, d}};
+    for (const Plane &q : in)
+        if (planes_clash(pr, q, T, e) || planes_clash(ph, q, T, e)) return LORA_ERR_INVALID_ARG;
+    if (planes_overlap(pr, ph, T, e)) return LORA_ERR_INVALID_ARG;
+    if (T == 0) return LORA_OK;
+    if ((rc = check_device(t))) return rc;
+    NormParams p = {};
+    p.ids = d_ids;
+    p.T = T;
+    p.d = d;
+    p.n = t->n;
+    p.x = z;
+    p.ldx = ldz;
+    if (norm) p.norm = *norm;
+    p.res = *res;
+    p.r = r;
+    p.ldr = ldr;
+    if (next) p.next = *next;
+    p.h = h;
+    p.ldh = ldh;
+    p.status = t->d_status;
+    return launch_block_norm(p, true, dt, static_cast<cudaStream_t>(stream));
 }
 
 int lora_get_status(const lora_table *t, uint32_t *h_status, int32_t reset, void *stream)

@@ -82,7 +82,7 @@ Options &options();
 // Host-side count of accepted launches per kernel (lora_kernel_launches).
 enum KernelKind {
     kKernDecode = 0, kKernCountSegments, kKernBuildSegments, kKernPrefillShrink, kKernPrefillExpand,
-    kKernBaseGemm, kKernMergeFinish, kKernKinds
+    kKernBaseGemm, kKernMergeFinish, kKernLayerShrink, kKernLayerStream, kKernLayerGemm, kKernBlockNorm, kKernKinds
 };
 void note_launch(KernelKind k);
 
@@ -106,6 +106,34 @@ int launch_base_gemm(const lora_table *t, const lora_segments *seg, const void *
 // y[t, y_off + n] = round(y[t, y_off + n] + yacc[t, n]) for t < T, n < o (merge.cu).
 int launch_merge_finish(void *y, int64_t ldy, int32_t y_off, const float *yacc, int64_t ldacc, int32_t T, int32_t o,
                         int dtype, cudaStream_t s);
+// Layer products with their epilogue (layer_gemm.cu, layer_stream.cu).  `epi` is never null here.
+// launch_layer_gemm: as launch_base_gemm, contiguous segments, v from launch_prefill_shrink.
+int launch_layer_gemm(const lora_table *t, const lora_segments *seg, const void *x, int64_t ldx, const void *W,
+                      int64_t ldw, const lora_epilogue *epi, void *y, int64_t ldy, int32_t y_off, const void *v,
+                      bool after_shrink, cudaStream_t s);
+// launch_layer_shrink: v[t, k] = s_i x[t] . A_i[k] (fp32) for per-token ids; launch_layer_stream:
+// the pass over W, with the adapter term from v when ids is not null.
+int launch_layer_shrink(const lora_table *t, const int32_t *ids, int32_t T, const void *x, int64_t ldx, float *v,
+                        int32_t ldv, cudaStream_t s);
+int launch_layer_stream(const lora_table *t, const int32_t *ids, int32_t T, const void *x, int64_t ldx, const void *W,
+                        int64_t ldw, const lora_epilogue *epi, void *y, int64_t ldy, int32_t y_off, const float *v,
+                        int32_t ldv, cudaStream_t s);
+// The norms around a block (block_norm.cu).
+struct NormParams {
+    const int32_t *ids;
+    int32_t T, d, n;
+    const void *x;         // the norm's input (z of the norm after)
+    int64_t ldx;
+    lora_norm norm;        // kind 0: none
+    lora_residual res;     // the norm after only
+    void *r;
+    int64_t ldr;
+    lora_norm next;        // kind 0: none
+    void *h;
+    int64_t ldh;
+    uint32_t *status;
+};
+int launch_block_norm(const NormParams &p, bool after, int dtype, cudaStream_t s);
 // Encode the TMA tensor map of A_i [rank, h] used by the decode shrink (host side).
 int encode_tmap_A(void *out128, const void *A, int dtype, int h, int rank);
 

@@ -31,7 +31,7 @@
  *
  * Streams.  Every call enqueues on the given CUDA stream (a cudaStream_t passed as void*;
  * NULL is the legacy default stream).  The hot calls (lora_build_segments, lora_shrink,
- * lora_expand, lora_sgmv, lora_bgmv) never allocate, never synchronise the host, and never
+ * lora_expand, lora_sgmv, lora_bgmv, the layer and norm calls) never allocate, never synchronise the host, and never
  * read device memory from the host.
  *
  * Errors.  Each call returns LORA_OK (0) or a negative LORA_ERR_* code.  Problems the host
@@ -234,6 +234,112 @@ int lora_bgmv_merged(const lora_table *table, const int32_t *d_ids, const float 
                      int32_t K, const void *x, int64_t ldx, void *y, int64_t ldy, int32_t y_offset,
                      void *ws, size_t ws_bytes, void *stream);
 
+/* What follows the product of a layer, on its fp32 sum z[t, n] and before the one rounding:
+ *   y[t, y_offset + n] = act(z[t, n] + bias[n]) * mul[t, n] + residual[t, n]
+ * with a null pointer leaving its step out.  bias is [o]; mul and residual are row-major [T, ld..]
+ * of the table's type, 16-byte aligned, ld.. >= o and a multiple of 8.  mul is the other half of a
+ * gated MLP (its up projection, when this call is the gate with LORA_ACT_SILU).  residual or mul
+ * may be the y slice itself (same address and row stride: an update in place); any other overlap
+ * of y with x, mul or residual is LORA_ERR_INVALID_ARG.  bias and W are weights: like a table's
+ * A_i and B_i they may be read ahead of the stream's earlier work, so a call of this library that
+ * is still in flight must not be writing them.
+ * The layer and norm calls want the table's device to be the current one (LORA_ERR_INVALID_ARG). */
+#define LORA_ACT_NONE 0
+#define LORA_ACT_RELU 1      /* max(z, 0)                                                        */
+#define LORA_ACT_GELU 2      /* z Phi(z), Phi the normal distribution function                   */
+#define LORA_ACT_GELU_TANH 3 /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2                  */
+#define LORA_ACT_SILU 4      /* z / (1 + exp(-z))                                                */
+typedef struct lora_epilogue {
+    const void *bias;
+    const void *mul;
+    const void *residual;
+    int64_t ldmul, ldres;
+    int32_t act;
+    int32_t reserved;
+} lora_epilogue;
+
+/* A whole layer in one pass: base weight, adapter term, bias, activation, gate product and
+ * residual ("TGI Multi-LoRA" page, "Technical Foundation: LoRA": W x + B A x; an activation can
+ * only follow their sum).
+ *   z[t, n] = sum_j x[t, j] W[n, j] + s_i * sum_k B_i[n, k] (x[t] . A_i[k])      (n < o)
+ * for every token t < seg->T; tokens outside all segments get the first sum only; then the
+ * epilogue above (NULL: y = z).  W and the requirements are those of lora_sgmv_base: a bf16 table
+ * whose ranks are multiples of 8 and at most 64 without Sigma, seg->perm == NULL, ws_bytes >=
+ * lora_workspace_bytes(table, T).  Two launches: the tcgen05 shrink, then a persistent tcgen05
+ * kernel that accumulates the base product and the adapter term in one tensor-memory tile.
+ * The scaled intermediate is kept as bf16 hi + lo (16 bits of mantissa); sums are fp32; y is
+ * rounded once. */
+int lora_sgmv_layer(const lora_table *table, const lora_segments *seg, const void *x, int64_t ldx,
+                    const void *W, int64_t ldw, const lora_epilogue *epilogue, void *y, int64_t ldy,
+                    int32_t y_offset, void *ws, size_t ws_bytes, void *stream);
+
+/* The same layer driven by per-token ids (decode: one token per request, any adapter each).
+ * d_ids is [T] on the device, -1 for no adapter; NULL: no token has one (then ws may be NULL).  An
+ * id outside [-1, n) latches LORA_STATUS_BAD_ID and leaves the token's row of y as it was.  A bf16
+ * table of any rank up to LORA_MAX_RANK, without Sigma (else LORA_ERR_UNSUPPORTED); ws_bytes >=
+ * lora_workspace_bytes(table, T).  Two launches (one without ids): the fp32 intermediate into the
+ * workspace, then one pass over W. */
+int lora_bgmv_layer(const lora_table *table, const int32_t *d_ids, int32_t T, const void *x,
+                    int64_t ldx, const void *W, int64_t ldw, const lora_epilogue *epilogue, void *y,
+                    int64_t ldy, int32_t y_offset, void *ws, size_t ws_bytes, void *stream);
+
+/* One normalisation over the d values of a row, in fp32:
+ *   LORA_NORM_RMS:   N(x) = x / sqrt(mean(x^2) + eps) * gain + shift
+ *   LORA_NORM_LAYER: N(x) = (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps) * gain + shift
+ * gain (NULL: 1) and shift (NULL: 0) are of the table's type, 16-byte aligned.  With ld == 0 they
+ * hold one row that serves every token.  With ld >= d (a multiple of 16 bytes) they hold 1 + n
+ * rows: row 0 the base model's and row 1 + i adapter i's, for adapters that train the norms with
+ * their A_i and B_i; a token with id i takes row 1 + i, one with id -1 (or a call without ids)
+ * row 0. */
+#define LORA_NORM_RMS 1
+#define LORA_NORM_LAYER 2
+typedef struct lora_norm {
+    const void *gain;
+    const void *shift;
+    int64_t ld;
+    float eps;      /* >= 0 and finite */
+    int32_t kind;
+} lora_norm;
+
+/* How a block's output joins the residual stream: r = res_scale * residual + branch_scale * gate * u.
+ * residual [T, ldres] (NULL: 0).  gate by kind: LORA_GATE_NONE 1; LORA_GATE_ADAPTER rows of
+ * ldgate elements chosen like a norm's gain (ldgate == 0: one row for all); LORA_GATE_TOKEN
+ * [T, ldgate], one row per token. */
+#define LORA_GATE_NONE 0
+#define LORA_GATE_ADAPTER 1
+#define LORA_GATE_TOKEN 2
+typedef struct lora_residual {
+    const void *residual;
+    const void *gate;
+    int64_t ldres, ldgate;
+    float res_scale, branch_scale;
+    int32_t gate_kind;
+    int32_t reserved;
+} lora_residual;
+
+/* Largest d of the two norm calls. */
+#define LORA_MAX_NORM_WIDTH 16384
+
+/* The norm before a block: h[t, 0:d] = N(x[t, 0:d]) for t < T.  The table gives the type (bf16 or
+ * fp32), the number of adapters and the status word; d need not be its h_in.  d_ids as in
+ * lora_bgmv_layer: a bad id latches LORA_STATUS_BAD_ID and leaves the token's row as it was.
+ * d and the row strides are multiples of 16 bytes, addresses 16-byte aligned.  h may be x (same
+ * address and stride); any other overlap is LORA_ERR_INVALID_ARG.  One launch, no workspace. */
+int lora_norm_before(const lora_table *table, const int32_t *d_ids, int32_t T, int32_t d,
+                     const void *x, int64_t ldx, const lora_norm *norm, void *h, int64_t ldh,
+                     void *stream);
+
+/* The norm after a block, its gate and scaled residual, and the next block's norm, in one pass:
+ *   u = N(z[t]) (norm NULL: z[t]);   r[t] = res_scale * residual[t] + branch_scale * gate * u;
+ *   h[t] = N_next(r[t])
+ * r (NULL: not wanted) and h (NULL together with next) are written once each, rounded from fp32;
+ * h is computed from the unrounded r.  At least one of r and h is given.  r and h may each be z,
+ * residual or a per-token gate (same address and stride), but not one another; any other overlap
+ * is LORA_ERR_INVALID_ARG.  Everything else as in lora_norm_before. */
+int lora_norm_after(const lora_table *table, const int32_t *d_ids, int32_t T, int32_t d,
+                    const void *z, int64_t ldz, const lora_norm *norm, const lora_residual *residual,
+                    void *r, int64_t ldr, const lora_norm *next, void *h, int64_t ldh, void *stream);
+
 /* Read (and with reset != 0, clear) the table's device status word into *h_status.
  * Synchronises `stream`.  Returns LORA_OK when the word is 0, LORA_ERR_TIMEOUT when the
  * timeout bit is set, otherwise LORA_ERR_DEVICE_STATUS. */
@@ -292,12 +398,12 @@ int lora_get_option(const char *key, int64_t *value);
  * kernels that the CUDA runtime has accepted since the library was loaded.  kind runs from 0 to
  * LORA_KERNEL_KINDS - 1 (0 the decode kernel, 1 and 2 the two segment-building kernels, 3 and
  * 4 the tcgen05 shrink and expand, 5 the fused base GEMM, 6 the merged ensembles' final
- * rounding).  lora_kernel_name returns the
- * kernel's name (static text; NULL outside that range) and lora_kernel_launches its count (-1
+ * rounding, 7 and 8 the shrink and the weight pass of lora_bgmv_layer, 9 the product of
+ * lora_sgmv_layer, 10 the norms).  lora_kernel_name returns the kernel's name (static text; NULL outside that range) and lora_kernel_launches its count (-1
  * outside that range).  A count says that a launch was enqueued, not that it has finished;
  * lora_get_status reports what the device found.  Tests read them to see which path a call
  * took. */
-#define LORA_KERNEL_KINDS 7
+#define LORA_KERNEL_KINDS 11
 const char *lora_kernel_name(int32_t kind);
 int64_t lora_kernel_launches(int32_t kind);
 

@@ -9,13 +9,15 @@
 // against 2 T h o flop: below ~250 tokens the tensor cores wait for memory), so it is built to keep
 // weight loads in flight: W takes the MMA's M side (128 rows of W a tile) and the tokens its N side
 // (16 to 256), so that no tensor-core row is spent on absent tokens, and the k axis of a tile is
-// split over the CTAs of a cluster where there are fewer tiles than SMs.  The CTAs' partial sums meet
-// through distributed shared memory and are added in CTA order (no atomics: bit-identical from run
-// to run).  The adapter term is added by the epilogue threads in fp32: a thread holds one output
-// column, so it reads its own row of B_i, and the token's v is the same for the whole warp.
+// split over the CTAs of a cluster where there are fewer tiles than SMs.  Each CTA finishes a share of the
+// tokens; the others send it their partial sums (st.async into its shared memory), which are added in a
+// fixed order (no atomics: bit-identical from run
+// to run).  The adapter term is formed by the epilogue warps in fp32 while W streams: a thread holds one
+// output column, so it reads its own row of B_i, and the token's v is the same for the whole warp; the
+// terms wait in tensor memory, in the columns behind the accumulator.
 //
-// Warp roles: warp 0 fills a ring of (W, x) k-blocks by TMA; warp 1 issues tcgen05.mma; warps 2..9
-// drain the accumulator (two per lane quarter), exchange it and finish the outputs.  Weight loads of
+// Warp roles: warp 0 fills a ring of (W, x) k-blocks by TMA; warp 1 issues tcgen05.mma; the others
+// drain the accumulator (one or two per lane quarter), exchange it and finish the outputs.  Weight loads of
 // the first stages are issued before the grid-dependency wait: W is never written by a call in flight.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -32,103 +34,7 @@
 namespace lora {
 namespace {
 
-// ------------------------------------------------------------------------------- shrink
-
-constexpr int kShrinkWarps = 8;
-
-struct LayerShrinkParams {
-    const AdapterDesc *desc;
-    const int32_t *ids;
-    const uint16_t *x;
-    int64_t ldx;
-    float *v;
-    int32_t ldv, n, h, split;   // split: warps that share one row of A_i (1, 2, 4 or 8)
-    uint32_t *status;
-};
-
-// Block (rank-row group, token).  A group of `split` warps forms one v[t, k]: 16-byte loads of x[t]
-// and A_i[k], fp32 sums folded by shuffles, then over the group's warps in their order.
-__global__ void __launch_bounds__(kShrinkWarps * 32) layer_shrink_kernel(const __grid_constant__ LayerShrinkParams p)
-{
-    __shared__ float part[kShrinkWarps];
-    // the wait comes first: launch_dependents then tells the pass over W that x and the epilogue's
-    // operands are final, and that only v is still to come
-    pdl_wait();
-    pdl_launch_dependents();
-    const int64_t t = blockIdx.y;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int a = p.ids[t];
-    if (a < 0 || a >= p.n) {
-        if (a != -1 && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.status, LORA_STATUS_BAD_ID);
-        return;
-    }
-    const int rank = p.desc[a].rank;
-    const int rows = kShrinkWarps / p.split;
-    const int k = blockIdx.x * rows + warp / p.split, sub = warp % p.split;
-    if (blockIdx.x * rows >= rank) return;   // the whole block
-    float s0 = 0.f, s1 = 0.f;
-    if (k < rank) {
-        const uint4 *xa = reinterpret_cast<const uint4 *>(p.x + t * p.ldx);
-        const uint4 *wa = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.desc[a].A) + (int64_t)k * p.h);
-        const int hv = p.h / 8;
-#pragma unroll 4
-        for (int j = sub * 32 + lane; j < hv; j += p.split * 32) {
-            const uint4 u = xa[j], w = wa[j];
-            const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                s0 = fmaf(bf16_lo(uu[i]), bf16_lo(ww[i]), s0);
-                s1 = fmaf(bf16_hi(uu[i]), bf16_hi(ww[i]), s1);
-            }
-        }
-    }
-    float s = s0 + s1;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    if (p.split > 1) {
-        if (lane == 0) part[warp] = s;
-        __syncthreads();
-        if (sub == 0)
-            for (int i = 1; i < p.split; ++i) s += part[warp + i];
-    }
-    if (lane == 0 && sub == 0 && k < rank) p.v[t * p.ldv + k] = s * p.desc[a].scale;
-}
-
-// ------------------------------------------------------------------------------- pass over W
-
-constexpr int kLM = 128;                      // rows of W per tile (MMA M)
-constexpr int kLK = 64;                       // k-block: one 128-byte swizzled row of bf16
-constexpr int kLWBytes = kLM * 128;
-constexpr int kLMaxN = 256;                   // tokens per tile (MMA N)
-constexpr int kLMaxStages = 8;
-constexpr int kLEpiWarps = 8;
-constexpr int kLThreads = (2 + kLEpiWarps) * 32;
-
-struct LayerStreamParams {
-    CUtensorMap tm_x;             // x [T, h], box 64 x N
-    CUtensorMap tm_w;             // W [o, h], box 64 x 128
-    const AdapterDesc *desc;
-    const int32_t *ids;           // null: no adapters
-    const float *v;               // [T, ldv] scaled intermediate
-    int32_t ldv, n;
-    int32_t T, h, o;
-    int32_t N, NT, stages;        // tokens per tile, token tiles, ring depth
-    int32_t early;                // launched right behind the shrink (see above)
-    uint16_t *y;                  // at column y_offset
-    int64_t ldy;
-    EpiParams epi;
-    uint32_t *status;
-    uint64_t wait_ns;
-};
-
-struct __align__(16) LayerStreamCtl {
-    uint64_t full[kLMaxStages], empty[kLMaxStages];
-    uint64_t done;
-    uint32_t tmem_base;
-    int32_t pad;
-    const void *B[kLMaxN];        // per token of this CTA's share: its B_i,
-    int32_t rank[kLMaxN];         // and rank (0: no adapter, -1: bad id)
-};
+// ------------------------------------------------------------------------------- clusters
 
 // Distributed-shared-memory address of `local` in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t map_cluster(uint32_t local, uint32_t rank)
@@ -145,38 +51,290 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr)
     return v;
 }
 
-// sum_k B_i[n, k] v[t, k] of one output; `row` is the row of B_i.
-__device__ __forceinline__ float expand_row(const uint16_t *row, const float *v, int rank)
+// ------------------------------------------------------------------------------- shrink
+
+constexpr int kShrinkWarps = 8;
+constexpr int kShrinkThreads = kShrinkWarps * 32;     // also the tokens that a cluster plans at a time
+constexpr int kShrinkRows = 16;                       // rank rows of a unit (mma M)
+constexpr int kShrinkTokens = 8;                      // tokens of a unit (mma N)
+constexpr int kShrinkK = 32;                          // k elements of one warp step
+
+struct LayerShrinkParams {
+    const AdapterDesc *desc;
+    const int32_t *ids;
+    const uint16_t *x;
+    int64_t ldx;
+    float *v;
+    int32_t ldv, n, h, T, width;   // width: CTAs of a cluster, which share a unit's k axis
+    uint32_t *status;
+};
+
+// D += A . B, 16 x 8 x 16.  The sum over k may be taken in any order, so the fragments are not laid out
+// by ldmatrix from shared memory but loaded from global memory as they lie: a lane's 16 bytes of row
+// (lane / 4) at k = 8 (lane % 4) are the k elements it holds in two of these products, the same ones in
+// A and in B.
+__device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                            uint32_t b1)
 {
-    float s0 = 0.f, s1 = 0.f;
-    if ((rank & 7) == 0) {   // the row is 16-byte aligned
-#pragma unroll 2
-        for (int k = 0; k < rank; k += 8) {
-            const uint4 b = *reinterpret_cast<const uint4 *>(row + k);
-            const float4 p = *reinterpret_cast<const float4 *>(v + k), q = *reinterpret_cast<const float4 *>(v + k + 4);
-            s0 = fmaf(bf16_lo(b.x), p.x, s0);
-            s1 = fmaf(bf16_hi(b.x), p.y, s1);
-            s0 = fmaf(bf16_lo(b.y), p.z, s0);
-            s1 = fmaf(bf16_hi(b.y), p.w, s1);
-            s0 = fmaf(bf16_lo(b.z), q.x, s0);
-            s1 = fmaf(bf16_hi(b.z), q.y, s1);
-            s0 = fmaf(bf16_lo(b.w), q.z, s0);
-            s1 = fmaf(bf16_hi(b.w), q.w, s1);
-        }
-    } else {
-        for (int k = 0; k < rank; ++k) s0 = fmaf(bf16_f(row[k]), v[k], s0);
-    }
-    return s0 + s1;
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <int S>   // CTAs per cluster that split the k axis
-__global__ void __launch_bounds__(kLThreads, 2) layer_stream_kernel(const __grid_constant__ LayerStreamParams p)
+// Token of the nth set bit of the window's mask, counting from 0; -1 when there are not that many.
+__device__ __forceinline__ int nth_member(const uint32_t *members, int nth, int w0)
 {
+    int tok = -1;
+#pragma unroll
+    for (int i = 0; i < kShrinkWarps; ++i) {
+        uint32_t m = members[i];
+        const int c = __popc(m);
+        if (tok < 0 && nth < c) {
+            for (int k = 0; k < nth; ++k) m &= m - 1;
+            tok = w0 + 32 * i + __ffs(m) - 1;
+        }
+        nth -= c;
+    }
+    return tok;
+}
+
+// A unit of work is up to 8 tokens of one adapter (found among 256 consecutive tokens) times 16 of its
+// rank rows, so a row of A_i is read once for 8 tokens and x once for 16 rows.  The reads bound it; the
+// products (2 T r h flop, a few percent of the pass over W) go to the warp-level tensor-core
+// instruction, whose operands need no shared memory here, so that all of the kernel's warps do nothing
+// but keep loads in flight.  The warps of a cluster share a unit's k axis in steps of 32; their partial
+// sums meet in shared memory and are added in warp and CTA order.
+__global__ void __launch_bounds__(kShrinkThreads, 2) layer_shrink_kernel(const __grid_constant__ LayerShrinkParams p)
+{
+    __shared__ __align__(16) int32_t ids[kShrinkThreads];
+    __shared__ int32_t first_unit[kShrinkThreads + 1];
+    __shared__ int32_t warp_units[kShrinkWarps];
+    __shared__ uint32_t members[kShrinkWarps];
+    __shared__ float part[kShrinkWarps][kShrinkRows * kShrinkTokens];
+    __shared__ float total_of[kShrinkRows * kShrinkTokens];   // this CTA's sum
+    // the wait comes first: launch_dependents then tells the pass over W that x and the epilogue's
+    // operands are final, and that only v is still to come
+    pdl_wait();
+    pdl_launch_dependents();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int crank = p.width > 1 ? (int)cluster_ctarank() : 0;
+    const int cluster = blockIdx.x / p.width, clusters = gridDim.x / p.width;
+    const int steps = (p.h + kShrinkK - 1) / kShrinkK, step0 = crank * kShrinkWarps + warp, dstep = p.width * kShrinkWarps;
+    const int row = lane >> 2, kl = (lane & 3) * 8;
+    int skipped = 0;   // units of the windows before
+    for (int w0 = 0; w0 < p.T; w0 += kShrinkThreads) {
+        // ---- the window's units, one token a thread
+        const int a = w0 + tid < p.T ? p.ids[w0 + tid] : -1;
+        const bool good = a >= 0 && a < p.n;
+        if (a != -1 && !good && blockIdx.x == 0) atomicOr(p.status, LORA_STATUS_BAD_ID);
+        ids[tid] = a;
+        const int rank_t = good ? p.desc[a].rank : 0;
+        __syncthreads();
+        // earlier tokens with the same adapter: of the warps before, then of this warp
+        int before = 0;
+        if (w0 + warp * 32 < p.T)
+#pragma unroll 8
+            for (int s = 0; s < warp * 32; s += 4) {
+                const int4 o = *reinterpret_cast<const int4 *>(ids + s);
+                before += (o.x == a) + (o.y == a) + (o.z == a) + (o.w == a);
+            }
+        before += __popc(__match_any_sync(0xffffffffu, a) & ((1u << lane) - 1));
+        const int units = before % kShrinkTokens == 0 ? (rank_t + kShrinkRows - 1) / kShrinkRows : 0;
+        int incl = units;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += o;
+        }
+        if (lane == 31) warp_units[warp] = incl;
+        __syncthreads();
+        int base = 0, total = 0;
+#pragma unroll
+        for (int i = 0; i < kShrinkWarps; ++i) {
+            if (i < warp) base += warp_units[i];
+            total += warp_units[i];
+        }
+        first_unit[tid] = base + incl - units;
+        if (tid == 0) first_unit[kShrinkThreads] = total;
+        __syncthreads();
+        // ---- every clusters-th unit
+        int u = cluster - skipped % clusters;
+        if (u < 0) u += clusters;
+        for (; u < total; u += clusters) {
+            int lo = 0, hi = kShrinkThreads;   // the last token whose first unit is at most u
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (first_unit[mid] <= u) lo = mid;
+                else hi = mid;
+            }
+            const int ad = ids[lo], k0 = (u - first_unit[lo]) * kShrinkRows;
+            const uint32_t vote = __ballot_sync(0xffffffffu, tid >= lo && ids[tid] == ad);
+            if (lane == 0) members[warp] = vote;
+            const AdapterDesc &d = p.desc[ad];
+            const int rank = d.rank;
+            __syncthreads();
+            const int tok = nth_member(members, row, w0);   // this lane's token column
+            const uint16_t *A = static_cast<const uint16_t *>(d.A);
+            const uint16_t *a0 = k0 + row < rank ? A + (int64_t)(k0 + row) * p.h + kl : nullptr;
+            const uint16_t *a1 = k0 + row + 8 < rank ? A + (int64_t)(k0 + row + 8) * p.h + kl : nullptr;
+            const uint16_t *xr = tok >= 0 ? p.x + tok * p.ldx + kl : nullptr;
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+            for (int j = step0; j < steps; j += dstep) {
+                const int k = j * kShrinkK;
+                const bool in = k + kl < p.h;   // h is a multiple of 8
+                const uint4 zero = make_uint4(0, 0, 0, 0);
+                const uint4 wa = in && a0 ? *reinterpret_cast<const uint4 *>(a0 + k) : zero;
+                const uint4 wb = in && a1 ? *reinterpret_cast<const uint4 *>(a1 + k) : zero;
+                const uint4 xv = in && xr ? *reinterpret_cast<const uint4 *>(xr + k) : zero;
+                mma_16x8x16(acc, wa.x, wb.x, wa.y, wb.y, xv.x, xv.y);
+                mma_16x8x16(acc, wa.z, wb.z, wa.w, wb.w, xv.z, xv.w);
+            }
+            // lane's outputs: rows lane / 4 and + 8, tokens 2 (lane % 4) and + 1
+            float *mine = part[warp] + row * kShrinkTokens + (lane & 3) * 2;
+            mine[0] = acc[0];
+            mine[1] = acc[1];
+            mine[8 * kShrinkTokens] = acc[2];
+            mine[8 * kShrinkTokens + 1] = acc[3];
+            __syncthreads();
+            float sum = 0.f;
+            if (tid < kShrinkRows * kShrinkTokens) {
+#pragma unroll
+                for (int i = 0; i < kShrinkWarps; ++i) sum += part[i][tid];
+                total_of[tid] = sum;
+            }
+            if (p.width > 1) cluster_sync_all();
+            if (crank == 0 && tid < kShrinkRows * kShrinkTokens) {
+                const int r = tid / kShrinkTokens, g = tid % kShrinkTokens;
+                if (p.width > 1) {
+                    float f[8];
+#pragma unroll
+                    for (int c = 1; c < 8; ++c) f[c] = c < p.width ? ld_cluster(map_cluster(smem_u32(&total_of[tid]), c)) : 0.f;
+#pragma unroll
+                    for (int c = 1; c < 8; ++c) sum += f[c];
+                }
+                const int at = nth_member(members, g, w0);
+                if (at >= 0 && k0 + r < rank) p.v[(int64_t)at * p.ldv + k0 + r] = sum * d.scale;
+            }
+            if (p.width > 1) cluster_sync_all();   // the sums are read before they are written again
+            else __syncthreads();
+        }
+        skipped += total;
+        __syncthreads();   // the plan is read by all before the next window's is written
+    }
+}
+
+// ------------------------------------------------------------------------------- pass over W
+
+constexpr int kLM = 128;                      // rows of W per tile (MMA M)
+constexpr int kLK = 64;                       // k-block: one 128-byte swizzled row of bf16
+constexpr int kLWBytes = kLM * 128;
+constexpr int kLMaxN = 256;                   // tokens per tile (MMA N)
+constexpr int kLMaxStages = 8;
+
+struct LayerStreamParams {
+    CUtensorMap tm_x;             // x [T, h], box 64 x N
+    CUtensorMap tm_w;             // W [o, h], box 64 x 128
+    const AdapterDesc *desc;
+    const int32_t *ids;           // null: no adapters
+    const float *v;               // [T, ldv] scaled intermediate
+    int32_t ldv, n;
+    int32_t T, h, o;
+    int32_t N, NT, stages;        // tokens per tile, token tiles, ring depth
+    int32_t share, ncols;         // tokens of a tile that one CTA of a cluster finishes, TMEM columns
+    int32_t recv;                 // offset in shared memory of the peers' partial sums
+    int32_t alias;                // they land in the ring
+    int32_t early;                // launched right behind the shrink (see above)
+    uint16_t *y;                  // at column y_offset
+    int64_t ldy;
+    EpiParams epi;
+    uint32_t *status;
+    uint64_t wait_ns;
+};
+
+struct __align__(16) LayerStreamCtl {
+    uint64_t full[kLMaxStages], empty[kLMaxStages];
+    uint64_t done, recv;
+    uint32_t tmem_base, pad[3];
+    // behind it: v of the tokens at hand (kLVBytes for each half of the epilogue warps), then per token of
+    // the share its B_i and its rank (0: no adapter, -1: bad id)
+};
+
+constexpr int kLBatch = 4;                    // tokens an epilogue thread works on at a time, their loads in flight
+// Bytes of v that a half of the epilogue warps holds at a time: at least a batch of tokens.
+constexpr int v_bytes(int epi_warps) { return epi_warps == 8 ? 8192 : 2048; }
+static_assert(v_bytes(4) / (LORA_MAX_RANK * 4) >= kLBatch, "a batch of tokens fits");
+
+// d[j] = sum_k B_j[n, k] v[j][k] for kLBatch tokens j; row[j] is row n of token j's B_i, v[j] its
+// intermediate (shared memory), rank[j] <= 0 for none.  Rows of a rank that is a multiple of 8 are
+// 16-byte aligned and read in 16-byte pieces, others element by element.
+__device__ __forceinline__ void expand_rows(const uint16_t *const (&row)[kLBatch], const float *const (&v)[kLBatch],
+                                            const int (&rank)[kLBatch], float (&d)[kLBatch])
+{
+    float s0[kLBatch], s1[kLBatch];
+    int even[kLBatch], odd[kLBatch], most_even = 0, most_odd = 0;
+#pragma unroll
+    for (int j = 0; j < kLBatch; ++j) {
+        s0[j] = s1[j] = 0.f;
+        even[j] = (rank[j] & 7) == 0 ? rank[j] : 0;
+        odd[j] = (rank[j] & 7) == 0 ? 0 : rank[j];
+        most_even = max(most_even, even[j]);
+        most_odd = max(most_odd, odd[j]);
+    }
+    for (int k = 0; k < most_even; k += 16) {
+        uint4 b[kLBatch][2];
+#pragma unroll
+        for (int j = 0; j < kLBatch; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (k + 8 * i < even[j]) b[j][i] = *reinterpret_cast<const uint4 *>(row[j] + k + 8 * i);
+#pragma unroll
+        for (int j = 0; j < kLBatch; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (k + 8 * i < even[j]) {
+                    const float4 p = *reinterpret_cast<const float4 *>(v[j] + k + 8 * i);
+                    const float4 q = *reinterpret_cast<const float4 *>(v[j] + k + 8 * i + 4);
+                    s0[j] = fmaf(bf16_lo(b[j][i].x), p.x, s0[j]);
+                    s1[j] = fmaf(bf16_hi(b[j][i].x), p.y, s1[j]);
+                    s0[j] = fmaf(bf16_lo(b[j][i].y), p.z, s0[j]);
+                    s1[j] = fmaf(bf16_hi(b[j][i].y), p.w, s1[j]);
+                    s0[j] = fmaf(bf16_lo(b[j][i].z), q.x, s0[j]);
+                    s1[j] = fmaf(bf16_hi(b[j][i].z), q.y, s1[j]);
+                    s0[j] = fmaf(bf16_lo(b[j][i].w), q.z, s0[j]);
+                    s1[j] = fmaf(bf16_hi(b[j][i].w), q.w, s1[j]);
+                }
+    }
+    for (int k = 0; k < most_odd; k += 4) {
+        uint16_t b[kLBatch][4];
+#pragma unroll
+        for (int j = 0; j < kLBatch; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[j][i] = k + i < odd[j] ? row[j][k + i] : (uint16_t)0;
+#pragma unroll
+        for (int j = 0; j < kLBatch; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (k + i < odd[j]) s0[j] = fmaf(bf16_f(b[j][i]), v[j][k + i], s0[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kLBatch; ++j) d[j] = s0[j] + s1[j];
+}
+
+// S CTAs of a cluster split the k axis; E epilogue warps (4 for small batches, so that three CTAs fit on
+// an SM and those of the next launch can fetch their weights while this one ends; else 8).
+template <int S, int E>
+__global__ void __launch_bounds__((2 + E) * 32, E == 4 ? 3 : 2)
+layer_stream_kernel(const __grid_constant__ LayerStreamParams p)
+{
+    constexpr int H = E / 4;   // epilogue warps per TMEM lane quarter, each with its part of the tokens
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int stage_bytes = kLWBytes + p.N * 128;
     LayerStreamCtl &ctl = *reinterpret_cast<LayerStreamCtl *>(ring + p.stages * stage_bytes);
-    float *part = reinterpret_cast<float *>(ring);   // [N][128] fp32 once the ring is done with
+    uint8_t *v_buf = reinterpret_cast<uint8_t *>(&ctl + 1);
+    const void **tok_B = reinterpret_cast<const void **>(v_buf + H * v_bytes(E));
+    int32_t *tok_rank = reinterpret_cast<int32_t *>(tok_B + p.share);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int crank = S > 1 ? (int)cluster_ctarank() : 0;
@@ -185,8 +343,9 @@ __global__ void __launch_bounds__(kLThreads, 2) layer_stream_kernel(const __grid
     const int row0 = mt * kLM, t0 = tt * p.N;
     const int nkb_all = (p.h + kLK - 1) / kLK;
     const int kb0 = (int)((int64_t)crank * nkb_all / S), nkb = (int)((int64_t)(crank + 1) * nkb_all / S) - kb0;
-    uint32_t ncols = 32;
-    while ((int)ncols < p.N) ncols *= 2;
+    // this CTA finishes tokens [ta, tb) of the tile
+    const int nv = min(p.N, p.T - t0);
+    const int ta = min(nv, crank * p.share), tb = min(nv, ta + p.share);
 
     if (tid == 0) {
         for (int i = 0; i < p.stages; ++i) {
@@ -194,10 +353,13 @@ __global__ void __launch_bounds__(kLThreads, 2) layer_stream_kernel(const __grid
             mbar_init(smem_u32(&ctl.empty[i]), 1);
         }
         mbar_init(smem_u32(&ctl.done), 1);
+        mbar_init(smem_u32(&ctl.recv), 1);
         fence_mbar_init_cluster();
+        // the partial sums of the other CTAs: 16 bytes per row of W and four tokens
+        if (S > 1) mbar_arrive_expect_tx(smem_u32(&ctl.recv), (uint32_t)((S - 1) * ((tb - ta + 3) / 4) * kLM * 16));
     }
     if (warp == 1) {
-        tmem_alloc(smem_u32(&ctl.tmem_base), ncols);
+        tmem_alloc(smem_u32(&ctl.tmem_base), (uint32_t)p.ncols);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -206,8 +368,10 @@ __global__ void __launch_bounds__(kLThreads, 2) layer_stream_kernel(const __grid
     // After the allocation: a dependent kernel's CTA on this SM cannot take the tensor memory that
     // this one is still waiting for.
     pdl_launch_dependents();
+    // The first cluster barrier says that a CTA may be sent partial sums: its barriers are set up, and
+    // where the sums land in the ring, its products are complete.
+    if (S > 1 && !p.alias) cluster_arrive_release();
     const uint32_t tmem = ctl.tmem_base;
-    bool ok = true;
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
@@ -236,7 +400,7 @@ __global__ void __launch_bounds__(kLThreads, 2) layer_stream_kernel(const __grid
             }
             __syncwarp();
         }
-        // drain: the copies of the last stages armed have landed before the ring is reused
+        // drain: the copies of the last stages armed have landed before the ring is given up
         if (lane == 0)
             for (int i = max(0, kb - p.stages); i < kb; ++i)
                 mbar_wait(smem_u32(&ctl.full[i % p.stages]), (i / p.stages) & 1, p.status, p.wait_ns);
@@ -256,20 +420,32 @@ __global__ void __launch_bounds__(kLThreads, 2) layer_stream_kernel(const __grid
                 umma_commit(smem_u32(&ctl.empty[s]));
             }
             umma_commit(smem_u32(&ctl.done));   // every MMA issued so far
+            mbar_wait(smem_u32(&ctl.done), 0, p.status, p.wait_ns);
         }
         __syncwarp();
     }
-    // This CTA's share of the tile's tokens, and their adapters.
-    const int nv = min(p.N, p.T - t0);
-    const int share = (nv + S - 1) / S;
-    const int ta = min(nv, crank * share), tb = min(nv, ta + share);
-    if (warp >= 2) {
+    if (warp < 2) {
+        if (S > 1) {
+            if (p.alias) cluster_arrive_release();
+            cluster_wait_acquire();
+            cluster_arrive_release();
+        }
+    } else {
+        // ------------------------------------------------------------ epilogue
+        // lane = row of W; this thread's tokens are [i0, i1) of the share
+        const int q = warp & 3, half = (warp - 2) >> 2, et = tid - 64;
+        const int m = q * 32 + lane, n = row0 + m;
+        const bool col_ok = n < p.o;
+        const int hs = (p.share / H + kLBatch - 1) / kLBatch * kLBatch;
+        const int i0 = half * hs, i1 = min(tb - ta, i0 + hs);
+        const uint32_t tmem_row = tmem + ((uint32_t)(q * 32) << 16);
+        const int64_t tok0 = t0 + ta;
         if (!p.early) pdl_wait();   // ids may come from the kernel before
-        for (int i = tid - 64; i < tb - ta; i += kLEpiWarps * 32) {
+        for (int i = et; i < tb - ta; i += E * 32) {
             int r = 0;
             const void *B = nullptr;
             if (p.ids) {
-                const int a = p.ids[t0 + ta + i];
+                const int a = p.ids[tok0 + i];
                 if (a >= 0 && a < p.n) {
                     r = p.desc[a].rank;
                     B = p.desc[a].B;
@@ -277,64 +453,135 @@ __global__ void __launch_bounds__(kLThreads, 2) layer_stream_kernel(const __grid
                     r = -1;
                 }
             }
-            ctl.rank[i] = r;
-            ctl.B[i] = B;
+            tok_rank[i] = r;
+            tok_B[i] = B;
         }
-    }
-    // Every thread learns whether the accumulator is complete; a wait that ran out anywhere in the
-    // CTA makes all of it skip the warp-collective loads (the cluster barriers are still met).
-    ok = mbar_wait(smem_u32(&ctl.done), 0, p.status, p.wait_ns);
-    ok = __syncthreads_and(ok) != 0;
-    tc_fence_after();
-    if (warp >= 2 && ok) {
-        // the partial sum, token by token, into the ring: lane = row of W
-        const int q = warp & 3, half = (warp - 2) >> 2;
-        for (int c = half * 16; c < p.N; c += 32) {
-            float f[16];
-            tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c, f);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) part[(c + i) * kLM + q * 32 + lane] = f[i];
+        const float bias = (col_ok && p.epi.bias) ? bf16_f(p.epi.bias[n]) : 0.f;
+        named_bar_sync(1, E * 32);
+        // what the steps below read goes to L2 while there is nothing else to do
+        const int rows_left = min(32, p.o - (n - lane));   // rows of this warp inside W
+        for (int i = i0; i < i1 && rows_left > 0; ++i) {
+            const int r = tok_rank[i];
+            const uint8_t *b = static_cast<const uint8_t *>(tok_B[i]) + (int64_t)(n - lane) * r * 2;
+            for (int off = lane * 128; off < rows_left * r * 2; off += 32 * 128) prefetch_l2(b + off);
+            if (lane == 0) {
+                if (p.epi.mul) prefetch_l2(p.epi.mul + (tok0 + i) * p.epi.ldmul + n);
+                if (p.epi.res) prefetch_l2(p.epi.res + (tok0 + i) * p.epi.ldres + n);
+            }
         }
-    }
-    tc_fence_before();
-    if (S > 1) cluster_sync_all();
-    else __syncthreads();
-    if (warp == 1) tmem_dealloc(tmem, ncols);
-    if (warp >= 2) {
+        // While W streams: bias and adapter term of every output, kept in tensor memory behind the
+        // accumulator.
         if (p.early) pdl_wait();   // v
-        const int e = tid - 64;
-        const int m = e & (kLM - 1), n = row0 + m;
-        const bool live = ok && n < p.o;
-        const float bias = (live && p.epi.bias) ? bf16_f(p.epi.bias[n]) : 0.f;
-        uint32_t peer[S];
+        float *vs = reinterpret_cast<float *>(v_buf + half * v_bytes(E));
+        const int at_once = p.ids ? v_bytes(E) / 4 / p.ldv / kLBatch * kLBatch : p.N;
+        for (int c = i0; c < i1; c += at_once) {
+            const int ce = min(i1, c + at_once);
+            if (p.ids) {
+                if (c > i0) named_bar_sync(2 + half, 128);   // the last tokens' v is done with
+                const float4 *src = reinterpret_cast<const float4 *>(p.v + (tok0 + c) * p.ldv);
+                for (int e = et & 127; e < (ce - c) * p.ldv / 4; e += 128) reinterpret_cast<float4 *>(vs)[e] = src[e];
+                named_bar_sync(2 + half, 128);
+            }
+            for (int i = c; i < ce; i += kLBatch) {
+                const uint16_t *row[kLBatch];
+                const float *v[kLBatch];
+                int r[kLBatch];
+                float d[kLBatch];
 #pragma unroll
-        for (int c = 0; c < S; ++c) peer[c] = S > 1 ? map_cluster(smem_u32(part), c) : smem_u32(part);
-        for (int i = e / kLM; i < tb - ta; i += kLEpiWarps * 32 / kLM) {
-            const int r = ctl.rank[i];
-            if (!live || r < 0) continue;
-            const int64_t t = t0 + ta + i;
-            float z[1] = {bias};
-#pragma unroll
-            for (int c = 0; c < S; ++c) z[0] += ld_cluster(peer[c] + (uint32_t)((ta + i) * kLM + m) * 4);
-            if (r > 0)
-                z[0] += expand_row(static_cast<const uint16_t *>(ctl.B[i]) + (int64_t)n * r, p.v + t * p.ldv, r);
-            activate(z, p.epi.act);
-            if (p.epi.mul) z[0] *= bf16_f(p.epi.mul[t * p.epi.ldmul + n]);
-            if (p.epi.res) z[0] += bf16_f(p.epi.res[t * p.epi.ldres + n]);
-            p.y[t * p.ldy + n] = __bfloat16_as_ushort(__float2bfloat16_rn(z[0]));
+                for (int j = 0; j < kLBatch; ++j) {
+                    const bool in = i + j < ce && col_ok;
+                    r[j] = in ? tok_rank[i + j] : 0;
+                    row[j] = in ? static_cast<const uint16_t *>(tok_B[i + j]) + (int64_t)n * r[j] : nullptr;
+                    v[j] = vs + (i + j - c) * p.ldv;
+                }
+                expand_rows(row, v, r, d);
+                __syncwarp();
+                tmem_st4(tmem_row + (uint32_t)(p.N + i), bias + d[0], bias + d[1], bias + d[2], bias + d[3]);
+            }
         }
+        // mul and residual of a batch, one ahead of its use
+        uint16_t mu[kLBatch], re[kLBatch];
+        auto operands = [&](int i) {
+#pragma unroll
+            for (int j = 0; j < kLBatch; ++j) {
+                const bool in = i + j < i1 && col_ok;
+                mu[j] = in && p.epi.mul ? p.epi.mul[(tok0 + i + j) * p.epi.ldmul + n] : (uint16_t)0;
+                re[j] = in && p.epi.res ? p.epi.res[(tok0 + i + j) * p.epi.ldres + n] : (uint16_t)0;
+            }
+        };
+        operands(i0);
+        // a wait that ran out makes the warp skip the rest, but not the cluster's barriers
+        bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&ctl.done), 0, p.status, p.wait_ns));
+        tc_fence_after();
+        const uint8_t *recv = ring + p.recv;
+        const int groups = p.share / 4;   // slots of four tokens per source
+        if (S > 1) {
+            if (p.alias) cluster_arrive_release();
+            cluster_wait_acquire();
+            // partial sums of the tokens that other CTAs finish, four tokens of a row at a time
+            for (int c = half * 16; ok && c < nv; c += 16 * H) {
+                float f[16];
+                tmem_ld16(tmem_row + (uint32_t)c, f);
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int tok = c + 4 * g, to = tok / p.share;
+                    if (tok >= nv || to == crank) continue;
+                    const int slot = (crank - to - 1 + S) % S;
+                    const uint32_t at = smem_u32(recv) + (uint32_t)(((slot * groups + (tok - to * p.share) / 4) * kLM + m) * 16);
+                    st_async_v4(at, smem_u32(&ctl.recv), (uint32_t)to,
+                                make_float4(f[4 * g], f[4 * g + 1], f[4 * g + 2], f[4 * g + 3]));
+                }
+            }
+            __syncwarp();
+            ok = __all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&ctl.recv), 0, p.status, p.wait_ns)) && ok;
+            cluster_arrive_release();   // nothing more comes to this CTA
+        }
+        for (int i = i0; ok && i < i1; i += kLBatch) {
+            float z[kLBatch], f[kLBatch];
+            tmem_ld4(tmem_row + (uint32_t)(p.N + i), z);
+            tmem_ld4(tmem_row + (uint32_t)(ta + i), f);
+            float4 o[S > 1 ? S - 1 : 1];
+#pragma unroll
+            for (int c = 0; c < S - 1; ++c)
+                o[c] = *reinterpret_cast<const float4 *>(recv + ((c * groups + i / 4) * kLM + m) * 16);
+#pragma unroll
+            for (int j = 0; j < kLBatch; ++j) z[j] += f[j];
+#pragma unroll
+            for (int c = 0; c < S - 1; ++c) {
+                z[0] += o[c].x;
+                z[1] += o[c].y;
+                z[2] += o[c].z;
+                z[3] += o[c].w;
+            }
+            activate(z, p.epi.act);
+#pragma unroll
+            for (int j = 0; j < kLBatch; ++j) {
+                if (p.epi.mul) z[j] *= bf16_f(mu[j]);
+                if (p.epi.res) z[j] += bf16_f(re[j]);
+            }
+            operands(i + kLBatch);
+#pragma unroll
+            for (int j = 0; j < kLBatch; ++j)
+                if (i + j < i1 && col_ok && tok_rank[i + j] >= 0)
+                    p.y[(tok0 + i + j) * p.ldy + n] = __bfloat16_as_ushort(__float2bfloat16_rn(z[j]));
+            __syncwarp();
+        }
+        tc_fence_before();
     }
-    if (S > 1) cluster_sync_all();   // no CTA leaves while a peer still reads its partial sums
+    if (S > 1) cluster_wait_acquire();   // no CTA leaves while it may still be sent something
+    __syncthreads();
+    if (warp == 1) tmem_dealloc(tmem, (uint32_t)p.ncols);
 }
 
 struct StreamShape {
-    int N, NT, S, stages, smem;
+    int N, NT, S, E, stages, share, ncols, recv, alias, smem;
 };
 
 // Tokens per tile: all of them up to 256 (rounded up to the MMA's 16), else equal tiles of at most
-// 256.  Clusters: as many CTAs splitting k as fill two CTAs per SM, up to 8.  Ring: half an SM's
-// shared memory, or all of it where a stage with its x tile leaves room for fewer than three stages
-// in half.
+// 256.  Clusters: as many CTAs splitting k as there is room for, up to 8.  CTAs per SM: three with four
+// epilogue warps for up to 32 tokens, two where half an SM's shared memory holds three stages and half
+// of its tensor memory the accumulator with the adapter terms behind it, else one.  One CTA alone
+// leaves 16 KB so that a CTA of the shrink fits beside it.
 StreamShape stream_shape(int T, int h, int o, int n_sms)
 {
     StreamShape sh;
@@ -342,31 +589,43 @@ StreamShape stream_shape(int T, int h, int o, int n_sms)
     const int per = (T + sh.NT - 1) / sh.NT;
     sh.N = (per + 15) & ~15;
     const int stage = kLWBytes + sh.N * 128;
-    const int ctl = (int)sizeof(LayerStreamCtl) + 1024;
-    const int half = 113 * 1024 - ctl, whole = 226 * 1024 - ctl;
-    const bool two = half / stage >= 3;
-    sh.stages = std::min(kLMaxStages, (two ? half : whole) / stage);
     const int64_t tiles = (int64_t)((o + kLM - 1) / kLM) * sh.NT;
-    const int64_t slots = (int64_t)n_sms * (two ? 2 : 1);
     const int nkb = (h + kLK - 1) / kLK;
-    sh.S = 1;
-    while (sh.S < 8 && tiles * sh.S * 2 <= slots && sh.S * 2 <= nkb) sh.S *= 2;
-    sh.smem = sh.stages * stage + ctl;
-    return sh;
+    for (int ctas = sh.N <= 32 ? 3 : 2;; --ctas) {
+        sh.E = sh.N <= 32 ? 4 : 8;
+        const int H = sh.E / 4;
+        sh.S = 1;
+        while (sh.S < 8 && tiles * sh.S * 2 <= (int64_t)n_sms * std::min(ctas, 2) && sh.S * 2 <= nkb) sh.S *= 2;
+        sh.share = ((std::min(sh.N, per) + sh.S - 1) / sh.S + kLBatch - 1) / kLBatch * kLBatch;
+        const int hs = (sh.share / H + kLBatch - 1) / kLBatch * kLBatch;
+        sh.ncols = 32;
+        while (sh.ncols < sh.N + H * hs) sh.ncols *= 2;
+        const int ctl = 1024 + (int)sizeof(LayerStreamCtl) + H * v_bytes(sh.E) + sh.share * 12;
+        const int recv = (sh.S - 1) * sh.share * kLM * 4;
+        const int room = (ctas == 1 ? 210 : 227 / ctas - 1) * 1024 - ctl;
+        sh.alias = sh.E == 8;
+        sh.stages = std::min(kLMaxStages, (room - (sh.alias ? 0 : recv)) / stage);
+        if (sh.alias && sh.stages * stage < recv) sh.stages = 0;
+        if (ctas > 1 && (sh.stages < 3 || sh.ncols > 512 / ctas)) continue;
+        sh.recv = sh.alias ? 0 : (sh.stages * stage + ctl - 1024 + 15) & ~15;
+        sh.smem = sh.stages * stage + ctl + (sh.alias ? 0 : recv + 16);
+        return sh;
+    }
 }
 
-template <int S>
+template <int S, int E>
 int launch_stream(const LayerStreamParams &p, const StreamShape &sh, cudaStream_t s, int dev)
 {
     static std::once_flag once[64];
     static cudaError_t attr_rc[64];
     std::call_once(once[dev], [&] {
-        attr_rc[dev] = cudaFuncSetAttribute(layer_stream_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
+        attr_rc[dev] =
+            cudaFuncSetAttribute(layer_stream_kernel<S, E>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     });
     if (attr_rc[dev] != cudaSuccess) return LORA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((int64_t)((p.o + kLM - 1) / kLM) * p.NT * S));
-    cfg.blockDim = dim3(kLThreads);
+    cfg.blockDim = dim3((2 + E) * 32);
     cfg.dynamicSmemBytes = (size_t)sh.smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -385,9 +644,20 @@ int launch_stream(const LayerStreamParams &p, const StreamShape &sh, cudaStream_
     }
     cfg.attrs = attr;
     cfg.numAttrs = na;
-    if (cudaLaunchKernelEx(&cfg, layer_stream_kernel<S>, p) != cudaSuccess) return LORA_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, layer_stream_kernel<S, E>, p) != cudaSuccess) return LORA_ERR_CUDA;
     note_launch(kKernLayerStream);
     return LORA_OK;
+}
+
+template <int E>
+int launch_stream_width(const LayerStreamParams &p, const StreamShape &sh, cudaStream_t s, int dev)
+{
+    switch (sh.S) {
+    case 8: return launch_stream<8, E>(p, sh, s, dev);
+    case 4: return launch_stream<4, E>(p, sh, s, dev);
+    case 2: return launch_stream<2, E>(p, sh, s, dev);
+    default: return launch_stream<1, E>(p, sh, s, dev);
+    }
 }
 
 int device_sms(int *dev, int *n_sms)
@@ -408,38 +678,51 @@ int launch_layer_shrink(const lora_table *t, const int32_t *ids, int32_t T, cons
 {
     int dev = 0, n_sms = 0;
     if (device_sms(&dev, &n_sms) != LORA_OK) return LORA_ERR_CUDA;
+    // The pass over W wants all of an SM's shared memory; with the same split of the SM's memory here its
+    // CTAs can join this kernel's on an SM instead of waiting for the SM to empty.
+    static std::once_flag once[64];
+    std::call_once(once[dev], [] {
+        cudaFuncSetAttribute(layer_shrink_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+    });
     LayerShrinkParams p;
     p.desc = t->d_desc;
-    p.x = static_cast<const uint16_t *>(x);
     p.ldx = ldx;
     p.ldv = ldv;
     p.n = t->n;
     p.h = t->h;
     p.status = t->d_status;
-    // Warps per row of A_i: several while there are fewer rows than warps to keep the SMs busy
-    // (and a row long enough to share).
-    p.split = 1;
-    while (p.split < kShrinkWarps && (int64_t)T * t->max_rank * p.split < 16ll * n_sms && t->h >= 256 * 2 * p.split)
-        p.split *= 2;
-    const int rows = kShrinkWarps / p.split;
-    for (int64_t t0 = 0; t0 < T; t0 += 65535) {   // gridDim.y
-        p.ids = ids + t0;
-        p.x = static_cast<const uint16_t *>(x) + t0 * ldx;
-        p.v = v + t0 * ldv;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)((t->max_rank + rows - 1) / rows), (unsigned)std::min<int64_t>(65535, T - t0));
-        cfg.blockDim = dim3(kShrinkWarps * 32);
-        cfg.stream = s;
-        cudaLaunchAttribute attr[1];
-        if (options().pdl) {
-            attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-            attr[0].val.programmaticStreamSerializationAllowed = 1;
-            cfg.numAttrs = 1;
-        }
-        cfg.attrs = attr;
-        if (cudaLaunchKernelEx(&cfg, layer_shrink_kernel, p) != cudaSuccess) return LORA_ERR_CUDA;
-        note_launch(kKernLayerShrink);
+    p.T = T;
+    p.ids = ids;
+    p.x = static_cast<const uint16_t *>(x);
+    p.v = v;
+    // CTAs that share a unit's k axis: as many, up to 8, as leave a CTA per SM (the largest rank taken for
+    // every token) and every warp a step.
+    const int64_t units = (int64_t)T * ((t->max_rank + kShrinkRows - 1) / kShrinkRows);
+    p.width = 1;
+    while (p.width < 8 && units * p.width * 2 <= n_sms && t->h >= 2 * p.width * kShrinkWarps * kShrinkK) p.width *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.width * std::min<int64_t>(units, 2 * n_sms / p.width)));
+    cfg.blockDim = dim3(kShrinkThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    int na = 0;
+    if (p.width > 1) {
+        attr[na].id = cudaLaunchAttributeClusterDimension;
+        attr[na].val.clusterDim.x = p.width;
+        attr[na].val.clusterDim.y = 1;
+        attr[na].val.clusterDim.z = 1;
+        ++na;
     }
+    if (options().pdl) {
+        attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[na].val.programmaticStreamSerializationAllowed = 1;
+        ++na;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = na;
+    if (cudaLaunchKernelEx(&cfg, layer_shrink_kernel, p) != cudaSuccess) return LORA_ERR_CUDA;
+    note_launch(kKernLayerShrink);
     return LORA_OK;
 }
 
@@ -466,18 +749,17 @@ int launch_layer_stream(const lora_table *t, const int32_t *ids, int32_t T, cons
     p.N = sh.N;
     p.NT = sh.NT;
     p.stages = sh.stages;
+    p.share = sh.share;
+    p.ncols = sh.ncols;
+    p.recv = sh.recv;
+    p.alias = sh.alias;
     p.early = (ids && options().pdl) ? 1 : 0;
     p.y = static_cast<uint16_t *>(y) + y_off;
     p.ldy = ldy;
     p.epi = epi_params(epi);
     p.status = t->d_status;
     p.wait_ns = wait_limit_ns();
-    switch (sh.S) {
-    case 8: return launch_stream<8>(p, sh, s, dev);
-    case 4: return launch_stream<4>(p, sh, s, dev);
-    case 2: return launch_stream<2>(p, sh, s, dev);
-    default: return launch_stream<1>(p, sh, s, dev);
-    }
+    return sh.E == 4 ? launch_stream_width<4>(p, sh, s, dev) : launch_stream_width<8>(p, sh, s, dev);
 }
 
 }  // namespace lora

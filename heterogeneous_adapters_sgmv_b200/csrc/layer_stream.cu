@@ -391,7 +391,7 @@ layer_stream_kernel(const __grid_constant__ LayerStreamParams p)
         int kb = pre;
         for (; kb < nkb; ++kb) {
             const int s = kb % p.stages, m = kb / p.stages;
-            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&ctl.empty[s]), (m - 1) & 1, p.status, p.wait_ns))) break;
+            if (!__all_sync(0xffffffffu, mbar_wait_hot(smem_u32(&ctl.empty[s]), (m - 1) & 1, p.status, p.wait_ns))) break;
             if (lane == 0) {
                 const uint32_t fb = smem_u32(&ctl.full[s]);
                 mbar_arrive_expect_tx(fb, (uint32_t)stage_bytes);
@@ -411,7 +411,7 @@ layer_stream_kernel(const __grid_constant__ LayerStreamParams p)
             const uint32_t idesc = idesc_bf16(kLM, p.N);
             for (int kb = 0; kb < nkb; ++kb) {
                 const int s = kb % p.stages, m = kb / p.stages;
-                if (!mbar_wait(smem_u32(&ctl.full[s]), m & 1, p.status, p.wait_ns)) break;
+                if (!mbar_wait_hot(smem_u32(&ctl.full[s]), m & 1, p.status, p.wait_ns)) break;
                 tc_fence_after();
                 const uint64_t wd = sw128_desc(smem_u32(ring + s * stage_bytes));
                 const uint64_t xd = sw128_desc(smem_u32(ring + s * stage_bytes + kLWBytes));

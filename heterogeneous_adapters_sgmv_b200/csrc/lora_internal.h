@@ -93,9 +93,10 @@ int launch_build_segments(const int32_t *ids, int32_t T, int32_t n, int32_t *per
 // Tensor maps of every adapter for the tcgen05 prefill path (no-op when the table does not qualify).
 int prefill_build_maps(lora_table *t);
 // tcgen05 shrink alone (contiguous segments, prefill-capable table): v receives the bf16 hi and
-// lo parts ([T, 64] each) of x . A_i^T, multiplied by s_i when fold_scale.
+// lo parts ([T, 64] each) of x . A_i^T, multiplied by s_i when fold_scale.  ksplit: 1 or 2 CTAs per
+// 128-token tile, or 0 for option "prefill_ksplit".
 int launch_prefill_shrink(const lora_table *t, const lora_segments *seg, const void *x, int64_t ldx, void *v,
-                          bool fold_scale, cudaStream_t s);
+                          bool fold_scale, int ksplit, cudaStream_t s);
 // Fused layer output (base_gemm.cu): y = (y if accumulate) + x W^T + the adapter term, from the
 // scale-folded intermediate v that launch_prefill_shrink wrote.
 // after_shrink: launch_prefill_shrink was the launch just before on `s` (lets the kernel start
@@ -149,7 +150,8 @@ struct lora_table {
     std::vector<float> scales;
     // per-adapter TMA tensor maps of A_i (device array of 128-byte CUtensorMap)
     void *d_tmaps;
-    // prefill path (bf16, ranks multiple of 8 and <= 64): 128-byte-swizzled maps of A_i, B_i
+    // prefill path (bf16, ranks multiple of 8 and <= 64): 128-byte-swizzled maps of A_i, B_i (of B_i n maps
+    // with 128-row boxes, then n with 64-row boxes)
     void *d_tmaps_pfA, *d_tmaps_pfB;
     // three-stage form: LORA_SIGMA_* and the per-adapter Sigma_i pointers (device, fp32)
     int32_t sigma_kind;

@@ -49,6 +49,18 @@ __device__ __forceinline__ void umma_commit(uint32_t bar)
                  : "memory");
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " elect.sync _|p, 0xffffffff;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok));
+    return ok != 0;
+}
+
 // ---- CTA pairs (cta_group::2): two CTAs of a cluster work on one tile.  Each holds its own half of
 // A's rows and of B's rows in its shared memory (same offsets in both), the even CTA issues.
 

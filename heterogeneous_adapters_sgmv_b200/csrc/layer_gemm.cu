@@ -225,25 +225,28 @@ __global__ void __launch_bounds__(kGThreads, 1) layer_gemm_kernel(const __grid_c
     // column tiles (read from DRAM once, then from L2) and all of x.
     if (warp == 0) {
         // ------------------------------------------------------------ producer
-        // One lane runs through the k-blocks (a k-block lasts 270 ns at the tensor cores' rate, and a loop
-        // with a division and warp votes in it took that long by itself); the warp meets for the segments.
+        // The whole warp runs the loops and one lane issues (see the issuer).
         const uint32_t empty0 = smem_u32(&ctl.empty[0]), full0 = smem_u32(&ctl.full[0]), lead0 = pair_leader(full0);
+        const uint32_t ring0 = smem_u32(ring);
+        const bool one = elect_one();
         int s = 0, used = 0;
         uint32_t phase = 1;   // the first pass finds every stage free
         bool ok = true, waited = !p.early;
-        auto next_stage = [&]() {
-            ++used;
+        auto free_stage = [&]() {
+            return __all_sync(0xffffffffu, mbar_wait_hot(empty0 + s * 8, phase, p.status, p.wait_ns)) != 0;
+        };
+        // a stage's two loads: this CTA's half of the A side and of the B side
+        auto load = [&](const void *ta, int ca, const void *tb, int cb, int row, int col) {
+            if (one) {
+                if (crank == 0) mbar_arrive_expect_tx(full0 + s * 8, 2 * kStage);
+                tma_load_2d_pair(ring0 + s * kStage, ta, ca, row, lead0 + s * 8);
+                tma_load_2d_pair(ring0 + s * kStage + kA, tb, cb, col, lead0 + s * 8);
+            }
+            if (used < STAGES) ++used;
             if (++s == STAGES) {
                 s = 0;
                 phase ^= 1;
             }
-        };
-        // a stage's two loads: this CTA's half of the A side and of the B side
-        auto load = [&](const void *ta, int ca, const void *tb, int cb, int row, int col) {
-            const uint32_t st = smem_u32(ring) + (uint32_t)(s * kStage);
-            if (crank == 0) mbar_arrive_expect_tx(full0 + s * 8, 2 * kStage);
-            tma_load_2d_pair(st, ta, ca, row, lead0 + s * 8);
-            tma_load_2d_pair(st + kA, tb, cb, col, lead0 + s * 8);
         };
         SegmentScan sc;
         sc.init(p);
@@ -252,16 +255,12 @@ __global__ void __launch_bounds__(kGThreads, 1) layer_gemm_kernel(const __grid_c
             int lo, hi, a;
             sc.begin(p, tile_row, tile_row + kGM);
             bool more = sc.next(p, &lo, &hi, &a);
-            if (lane == 0) {
-                for (int kb = 0; kb < nkb; ++kb) {
-                    ok = mbar_wait_hot(empty0 + s * 8, phase, p.status, p.wait_ns);
-                    if (!ok) break;
-                    if (kb + 1 == nkb) ctl.last[s] = !more;
-                    load(&p.tm_x, kb * kGK, &p.tm_w, kb * kGK, row, col);
-                    next_stage();
-                }
+            for (int kb = 0; kb < nkb; ++kb) {
+                ok = free_stage();
+                if (!ok) break;
+                if (kb + 1 == nkb && one) ctl.last[s] = !more;
+                load(&p.tm_x, kb * kGK, &p.tm_w, kb * kGK, row, col);
             }
-            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
             while (ok && more) {
                 if (!waited) {
                     pdl_wait();
@@ -270,35 +269,31 @@ __global__ void __launch_bounds__(kGThreads, 1) layer_gemm_kernel(const __grid_c
                 const int lo1 = lo, hi1 = hi;
                 const void *tb = p.tm_B + (size_t)a * 128;
                 more = sc.next(p, &lo, &hi, &a);
-                if (lane == 0) {
-                    for (int part = 0; part < 2; ++part) {   // hi, lo
-                        ok = mbar_wait_hot(empty0 + s * 8, phase, p.status, p.wait_ns);
-                        if (!ok) break;
+                for (int part = 0; part < 2; ++part) {   // hi, lo
+                    ok = free_stage();
+                    if (!ok) break;
+                    if (one) {
                         ctl.lo[s] = (int16_t)lo1;
                         ctl.hi[s] = (int16_t)hi1;
                         ctl.last[s] = part == 1 && !more;
-                        load(part ? &p.tm_vlo : &p.tm_vhi, 0, tb, 0, row, col);
-                        next_stage();
                     }
+                    load(part ? &p.tm_vlo : &p.tm_vhi, 0, tb, 0, row, col);
                 }
-                ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
             }
         }
         if (!waited) pdl_wait();   // this grid never completes before the shrink
         // drain: the copies of the last stages have landed in both CTAs before either leaves (earlier
         // ones were consumed before their stage was loaded again)
-        if (lane == 0) {
-            if (crank == 0) {
-                for (int i = 0; i < min(used, STAGES); ++i) {   // newest first
-                    if (--s < 0) {
-                        s = STAGES - 1;
-                        phase ^= 1;
-                    }
-                    mbar_wait(full0 + s * 8, phase ^ 1, p.status, p.wait_ns);
+        if (crank == 0) {
+            for (int i = 0; i < used; ++i) {   // newest first
+                if (--s < 0) {
+                    s = STAGES - 1;
+                    phase ^= 1;
                 }
-            } else if (!ok) {
-                __nanosleep(1000000);   // a wait ran out: let this CTA's own copies land
+                mbar_wait(full0 + s * 8, phase ^ 1, p.status, p.wait_ns);
             }
+        } else if (!ok) {
+            __nanosleep(1000000);   // a wait ran out: let this CTA's own copies land
         }
         __syncwarp();
     } else if (warp == 1) {

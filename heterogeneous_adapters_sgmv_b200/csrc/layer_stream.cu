@@ -375,53 +375,62 @@ layer_stream_kernel(const __grid_constant__ LayerStreamParams p)
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
+        // The whole warp runs the loop and one lane issues: the copy and MMA instructions take their operands
+        // from uniform registers, which a loop inside one lane has to move them to one by one.
+        const uint32_t ring0 = smem_u32(ring), full0 = smem_u32(&ctl.full[0]), empty0 = smem_u32(&ctl.empty[0]);
+        const bool one = elect_one();
         const int pre = min(nkb, p.stages);
-        if (lane == 0) {
+        if (one)
             for (int kb = 0; kb < pre; ++kb) {
-                const uint32_t fb = smem_u32(&ctl.full[kb]);
-                mbar_arrive_expect_tx(fb, (uint32_t)stage_bytes);
-                tma_load_2d(smem_u32(ring + kb * stage_bytes), &p.tm_w, (kb0 + kb) * kLK, row0, fb);
+                mbar_arrive_expect_tx(full0 + kb * 8, (uint32_t)stage_bytes);
+                tma_load_2d(ring0 + kb * stage_bytes, &p.tm_w, (kb0 + kb) * kLK, row0, full0 + kb * 8);
             }
-            if (!p.early) pdl_wait();
+        if (!p.early) pdl_wait();
+        if (one)
             for (int kb = 0; kb < pre; ++kb)
-                tma_load_2d(smem_u32(ring + kb * stage_bytes + kLWBytes), &p.tm_x, (kb0 + kb) * kLK, t0,
-                            smem_u32(&ctl.full[kb]));
-        }
-        __syncwarp();
-        int kb = pre;
+                tma_load_2d(ring0 + kb * stage_bytes + kLWBytes, &p.tm_x, (kb0 + kb) * kLK, t0, full0 + kb * 8);
+        int kb = pre, s = pre == p.stages ? 0 : pre;
+        uint32_t phase = 0;
         for (; kb < nkb; ++kb) {
-            const int s = kb % p.stages, m = kb / p.stages;
-            if (!__all_sync(0xffffffffu, mbar_wait_hot(smem_u32(&ctl.empty[s]), (m - 1) & 1, p.status, p.wait_ns))) break;
-            if (lane == 0) {
-                const uint32_t fb = smem_u32(&ctl.full[s]);
-                mbar_arrive_expect_tx(fb, (uint32_t)stage_bytes);
-                tma_load_2d(smem_u32(ring + s * stage_bytes), &p.tm_w, (kb0 + kb) * kLK, row0, fb);
-                tma_load_2d(smem_u32(ring + s * stage_bytes + kLWBytes), &p.tm_x, (kb0 + kb) * kLK, t0, fb);
+            if (!__all_sync(0xffffffffu, mbar_wait_hot(empty0 + s * 8, phase, p.status, p.wait_ns))) break;
+            if (one) {
+                mbar_arrive_expect_tx(full0 + s * 8, (uint32_t)stage_bytes);
+                tma_load_2d(ring0 + s * stage_bytes, &p.tm_w, (kb0 + kb) * kLK, row0, full0 + s * 8);
+                tma_load_2d(ring0 + s * stage_bytes + kLWBytes, &p.tm_x, (kb0 + kb) * kLK, t0, full0 + s * 8);
             }
-            __syncwarp();
+            if (++s == p.stages) {
+                s = 0;
+                phase ^= 1;
+            }
         }
         // drain: the copies of the last stages armed have landed before the ring is given up
-        if (lane == 0)
-            for (int i = max(0, kb - p.stages); i < kb; ++i)
-                mbar_wait(smem_u32(&ctl.full[i % p.stages]), (i / p.stages) & 1, p.status, p.wait_ns);
+        for (int i = max(0, kb - p.stages); i < kb; ++i)
+            mbar_wait(full0 + i % p.stages * 8, (i / p.stages) & 1, p.status, p.wait_ns);
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            const uint32_t idesc = idesc_bf16(kLM, p.N);
-            for (int kb = 0; kb < nkb; ++kb) {
-                const int s = kb % p.stages, m = kb / p.stages;
-                if (!mbar_wait_hot(smem_u32(&ctl.full[s]), m & 1, p.status, p.wait_ns)) break;
-                tc_fence_after();
-                const uint64_t wd = sw128_desc(smem_u32(ring + s * stage_bytes));
-                const uint64_t xd = sw128_desc(smem_u32(ring + s * stage_bytes + kLWBytes));
+        const uint32_t idesc = idesc_bf16(kLM, p.N);
+        const uint32_t full0 = smem_u32(&ctl.full[0]), empty0 = smem_u32(&ctl.empty[0]);
+        const uint64_t wd0 = sw128_desc(smem_u32(ring)), xd0 = sw128_desc(smem_u32(ring) + kLWBytes);
+        const bool one = elect_one();
+        int s = 0;
+        uint32_t phase = 0;
+        for (int kb = 0; kb < nkb; ++kb) {
+            if (!__all_sync(0xffffffffu, mbar_wait_hot(full0 + s * 8, phase, p.status, p.wait_ns))) break;
+            tc_fence_after();
+            const uint64_t wd = wd0 + (uint64_t)(s * (stage_bytes >> 4)), xd = xd0 + (uint64_t)(s * (stage_bytes >> 4));
+            if (one) {
 #pragma unroll
                 for (int k = 0; k < kLK / 16; ++k) umma_bf16(tmem, wd + 2 * k, xd + 2 * k, idesc, (kb | k) != 0 ? 1u : 0u);
-                umma_commit(smem_u32(&ctl.empty[s]));
+                umma_commit(empty0 + s * 8);
             }
-            umma_commit(smem_u32(&ctl.done));   // every MMA issued so far
-            mbar_wait(smem_u32(&ctl.done), 0, p.status, p.wait_ns);
+            if (++s == p.stages) {
+                s = 0;
+                phase ^= 1;
+            }
         }
+        if (one) umma_commit(smem_u32(&ctl.done));   // every MMA issued so far
+        mbar_wait(smem_u32(&ctl.done), 0, p.status, p.wait_ns);
         __syncwarp();
     }
     if (warp < 2) {

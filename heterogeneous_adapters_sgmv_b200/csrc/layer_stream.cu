@@ -34,23 +34,6 @@
 namespace lora {
 namespace {
 
-// ------------------------------------------------------------------------------- clusters
-
-// Distributed-shared-memory address of `local` in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t map_cluster(uint32_t local, uint32_t rank)
-{
-    uint32_t remote;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
-    return remote;
-}
-
-__device__ __forceinline__ float ld_cluster(uint32_t addr)
-{
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
-}
-
 // ------------------------------------------------------------------------------- shrink
 
 constexpr int kShrinkWarps = 8;
@@ -58,14 +41,15 @@ constexpr int kShrinkThreads = kShrinkWarps * 32;     // also the tokens that a 
 constexpr int kShrinkRows = 16;                       // rank rows of a unit (mma M)
 constexpr int kShrinkTokens = 8;                      // tokens of a unit (mma N)
 constexpr int kShrinkK = 32;                          // k elements of one warp step
+constexpr int kVParts = 8;                            // parts of the k axis, at most
 
 struct LayerShrinkParams {
     const AdapterDesc *desc;
     const int32_t *ids;
     const uint16_t *x;
     int64_t ldx;
-    float *v;
-    int32_t ldv, n, h, T, width;   // width: CTAs of a cluster, which share a unit's k axis
+    float *v;                      // [parts][T, ldv]
+    int32_t ldv, n, h, T, parts;   // parts: pieces of the k axis, summed by the reader of v
     uint32_t *status;
 };
 
@@ -99,36 +83,38 @@ __device__ __forceinline__ int nth_member(const uint32_t *members, int nth, int 
 }
 
 // A unit of work is up to 8 tokens of one adapter (found among 256 consecutive tokens) times 16 of its
-// rank rows, so a row of A_i is read once for 8 tokens and x once for 16 rows.  The reads bound it; the
-// products (2 T r h flop, a few percent of the pass over W) go to the warp-level tensor-core
-// instruction, whose operands need no shared memory here, so that all of the kernel's warps do nothing
-// but keep loads in flight.  The warps of a cluster share a unit's k axis in steps of 32; their partial
-// sums meet in shared memory and are added in warp and CTA order.
+// rank rows times one part of the k axis, so a row of A_i is read once for 8 tokens and x once for 16
+// rows.  The reads bound it; the products (2 T r h flop, a few percent of the pass over W) go to the
+// warp-level tensor-core instruction, whose operands need no shared memory here, so that all of the
+// kernel's warps do nothing but keep loads in flight.  The parts of the k axis are sized for about four
+// steps a warp and go to memory one by one (the pass over W adds them up as it reads them): in a small
+// batch the time is a chain of dependent loads, and every step or barrier more is felt (one token: ids,
+// descriptor, A_i and x, store).
 __global__ void __launch_bounds__(kShrinkThreads, 2) layer_shrink_kernel(const __grid_constant__ LayerShrinkParams p)
 {
     __shared__ __align__(16) int32_t ids[kShrinkThreads];
-    __shared__ int32_t first_unit[kShrinkThreads + 1];
+    __shared__ AdapterDesc desc[kShrinkThreads];
+    __shared__ int32_t first_unit[kShrinkThreads];
     __shared__ int32_t warp_units[kShrinkWarps];
     __shared__ uint32_t members[kShrinkWarps];
     __shared__ float part[kShrinkWarps][kShrinkRows * kShrinkTokens];
-    __shared__ float total_of[kShrinkRows * kShrinkTokens];   // this CTA's sum
     // the wait comes first: launch_dependents then tells the pass over W that x and the epilogue's
     // operands are final, and that only v is still to come
     pdl_wait();
     pdl_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int crank = p.width > 1 ? (int)cluster_ctarank() : 0;
-    const int cluster = blockIdx.x / p.width, clusters = gridDim.x / p.width;
-    const int steps = (p.h + kShrinkK - 1) / kShrinkK, step0 = crank * kShrinkWarps + warp, dstep = p.width * kShrinkWarps;
+    const int steps = (p.h + kShrinkK - 1) / kShrinkK;
     const int row = lane >> 2, kl = (lane & 3) * 8;
-    int skipped = 0;   // units of the windows before
+    int64_t item = blockIdx.x;   // counts the items of all windows
+    int64_t skipped = 0;
     for (int w0 = 0; w0 < p.T; w0 += kShrinkThreads) {
         // ---- the window's units, one token a thread
         const int a = w0 + tid < p.T ? p.ids[w0 + tid] : -1;
         const bool good = a >= 0 && a < p.n;
         if (a != -1 && !good && blockIdx.x == 0) atomicOr(p.status, LORA_STATUS_BAD_ID);
+        AdapterDesc mine = {};
+        if (good) mine = p.desc[a];
         ids[tid] = a;
-        const int rank_t = good ? p.desc[a].rank : 0;
         __syncthreads();
         // earlier tokens with the same adapter: of the warps before, then of this warp
         int before = 0;
@@ -139,7 +125,8 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) layer_shrink_kernel(const _
                 before += (o.x == a) + (o.y == a) + (o.z == a) + (o.w == a);
             }
         before += __popc(__match_any_sync(0xffffffffu, a) & ((1u << lane) - 1));
-        const int units = before % kShrinkTokens == 0 ? (rank_t + kShrinkRows - 1) / kShrinkRows : 0;
+        const int units = good && before % kShrinkTokens == 0 ? (mine.rank + kShrinkRows - 1) / kShrinkRows : 0;
+        desc[tid] = mine;
         int incl = units;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -148,39 +135,31 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) layer_shrink_kernel(const _
         }
         if (lane == 31) warp_units[warp] = incl;
         __syncthreads();
-        int base = 0, total = 0;
+        int first = incl - units, total = 0;
 #pragma unroll
         for (int i = 0; i < kShrinkWarps; ++i) {
-            if (i < warp) base += warp_units[i];
+            if (i < warp) first += warp_units[i];
             total += warp_units[i];
         }
-        first_unit[tid] = base + incl - units;
-        if (tid == 0) first_unit[kShrinkThreads] = total;
-        __syncthreads();
-        // ---- every clusters-th unit
-        int u = cluster - skipped % clusters;
-        if (u < 0) u += clusters;
-        for (; u < total; u += clusters) {
-            int lo = 0, hi = kShrinkThreads;   // the last token whose first unit is at most u
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (first_unit[mid] <= u) lo = mid;
-                else hi = mid;
-            }
+        first_unit[tid] = first;
+        // ---- every gridDim.x-th item
+        for (; item - skipped < (int64_t)total * p.parts; item += gridDim.x) {
+            const int u = (int)((item - skipped) / p.parts), ks = (int)((item - skipped) % p.parts);
+            const int lo = __syncthreads_count(first <= u) - 1;   // the token that leads the unit
             const int ad = ids[lo], k0 = (u - first_unit[lo]) * kShrinkRows;
-            const uint32_t vote = __ballot_sync(0xffffffffu, tid >= lo && ids[tid] == ad);
+            const uint32_t vote = __ballot_sync(0xffffffffu, tid >= lo && a == ad);
             if (lane == 0) members[warp] = vote;
-            const AdapterDesc &d = p.desc[ad];
-            const int rank = d.rank;
+            const int rank = desc[lo].rank;
+            const uint16_t *A = static_cast<const uint16_t *>(desc[lo].A);
             __syncthreads();
             const int tok = nth_member(members, row, w0);   // this lane's token column
-            const uint16_t *A = static_cast<const uint16_t *>(d.A);
             const uint16_t *a0 = k0 + row < rank ? A + (int64_t)(k0 + row) * p.h + kl : nullptr;
             const uint16_t *a1 = k0 + row + 8 < rank ? A + (int64_t)(k0 + row + 8) * p.h + kl : nullptr;
             const uint16_t *xr = tok >= 0 ? p.x + tok * p.ldx + kl : nullptr;
+            const int s1 = (int)((int64_t)(ks + 1) * steps / p.parts);
             float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-            for (int j = step0; j < steps; j += dstep) {
+            for (int j = (int)((int64_t)ks * steps / p.parts) + warp; j < s1; j += kShrinkWarps) {
                 const int k = j * kShrinkK;
                 const bool in = k + kl < p.h;   // h is a multiple of 8
                 const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -191,35 +170,21 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) layer_shrink_kernel(const _
                 mma_16x8x16(acc, wa.z, wb.z, wa.w, wb.w, xv.z, xv.w);
             }
             // lane's outputs: rows lane / 4 and + 8, tokens 2 (lane % 4) and + 1
-            float *mine = part[warp] + row * kShrinkTokens + (lane & 3) * 2;
-            mine[0] = acc[0];
-            mine[1] = acc[1];
-            mine[8 * kShrinkTokens] = acc[2];
-            mine[8 * kShrinkTokens + 1] = acc[3];
+            float *out = part[warp] + row * kShrinkTokens + (lane & 3) * 2;
+            out[0] = acc[0];
+            out[1] = acc[1];
+            out[8 * kShrinkTokens] = acc[2];
+            out[8 * kShrinkTokens + 1] = acc[3];
             __syncthreads();
-            float sum = 0.f;
             if (tid < kShrinkRows * kShrinkTokens) {
+                const int r = tid / kShrinkTokens, at = nth_member(members, tid % kShrinkTokens, w0);
+                float sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < kShrinkWarps; ++i) sum += part[i][tid];
-                total_of[tid] = sum;
+                if (at >= 0 && k0 + r < rank) p.v[((int64_t)ks * p.T + at) * p.ldv + k0 + r] = sum * desc[lo].scale;
             }
-            if (p.width > 1) cluster_sync_all();
-            if (crank == 0 && tid < kShrinkRows * kShrinkTokens) {
-                const int r = tid / kShrinkTokens, g = tid % kShrinkTokens;
-                if (p.width > 1) {
-                    float f[8];
-#pragma unroll
-                    for (int c = 1; c < 8; ++c) f[c] = c < p.width ? ld_cluster(map_cluster(smem_u32(&total_of[tid]), c)) : 0.f;
-#pragma unroll
-                    for (int c = 1; c < 8; ++c) sum += f[c];
-                }
-                const int at = nth_member(members, g, w0);
-                if (at >= 0 && k0 + r < rank) p.v[(int64_t)at * p.ldv + k0 + r] = sum * d.scale;
-            }
-            if (p.width > 1) cluster_sync_all();   // the sums are read before they are written again
-            else __syncthreads();
         }
-        skipped += total;
+        skipped += (int64_t)total * p.parts;
         __syncthreads();   // the plan is read by all before the next window's is written
     }
 }
@@ -237,7 +202,8 @@ struct LayerStreamParams {
     CUtensorMap tm_w;             // W [o, h], box 64 x 128
     const AdapterDesc *desc;
     const int32_t *ids;           // null: no adapters
-    const float *v;               // [T, ldv] scaled intermediate
+    const float *v;               // [v_parts][T, ldv]: the scaled intermediate is their sum
+    int32_t v_parts;
     int32_t ldv, n;
     int32_t T, h, o;
     int32_t N, NT, stages;        // tokens per tile, token tiles, ring depth
@@ -488,7 +454,21 @@ layer_stream_kernel(const __grid_constant__ LayerStreamParams p)
             if (p.ids) {
                 if (c > i0) named_bar_sync(2 + half, 128);   // the last tokens' v is done with
                 const float4 *src = reinterpret_cast<const float4 *>(p.v + (tok0 + c) * p.ldv);
-                for (int e = et & 127; e < (ce - c) * p.ldv / 4; e += 128) reinterpret_cast<float4 *>(vs)[e] = src[e];
+                for (int e = et & 127; e < (ce - c) * p.ldv / 4; e += 128) {
+                    float4 f[kVParts];
+#pragma unroll
+                    for (int k = 0; k < kVParts; ++k)
+                        if (k < p.v_parts) f[k] = src[e + (int64_t)k * p.T * (p.ldv / 4)];
+#pragma unroll
+                    for (int k = 1; k < kVParts; ++k)
+                        if (k < p.v_parts) {
+                            f[0].x += f[k].x;
+                            f[0].y += f[k].y;
+                            f[0].z += f[k].z;
+                            f[0].w += f[k].w;
+                        }
+                    reinterpret_cast<float4 *>(vs)[e] = f[0];
+                }
                 named_bar_sync(2 + half, 128);
             }
             for (int i = c; i < ce; i += kLBatch) {
@@ -682,6 +662,12 @@ int device_sms(int *dev, int *n_sms)
 
 }  // namespace
 
+int layer_v_parts(int32_t T, int32_t h)
+{
+    if (T > kLayerPartTokens) return 1;   // enough units without
+    return std::min(kVParts, std::max(1, h / (kShrinkK * kShrinkWarps * 4)));
+}
+
 int launch_layer_shrink(const lora_table *t, const int32_t *ids, int32_t T, const void *x, int64_t ldx, float *v,
                         int32_t ldv, cudaStream_t s)
 {
@@ -705,31 +691,19 @@ int launch_layer_shrink(const lora_table *t, const int32_t *ids, int32_t T, cons
     p.ids = ids;
     p.x = static_cast<const uint16_t *>(x);
     p.v = v;
-    // CTAs that share a unit's k axis: as many, up to 8, as leave a CTA per SM (the largest rank taken for
-    // every token) and every warp a step.
-    const int64_t units = (int64_t)T * ((t->max_rank + kShrinkRows - 1) / kShrinkRows);
-    p.width = 1;
-    while (p.width < 8 && units * p.width * 2 <= n_sms && t->h >= 2 * p.width * kShrinkWarps * kShrinkK) p.width *= 2;
+    p.parts = layer_v_parts(T, t->h);
+    const int64_t items = (int64_t)T * ((t->max_rank + kShrinkRows - 1) / kShrinkRows) * p.parts;   // at most
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.width * std::min<int64_t>(units, 2 * n_sms / p.width)));
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>(items, 2 * n_sms));
     cfg.blockDim = dim3(kShrinkThreads);
     cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    int na = 0;
-    if (p.width > 1) {
-        attr[na].id = cudaLaunchAttributeClusterDimension;
-        attr[na].val.clusterDim.x = p.width;
-        attr[na].val.clusterDim.y = 1;
-        attr[na].val.clusterDim.z = 1;
-        ++na;
-    }
+    cudaLaunchAttribute attr[1];
     if (options().pdl) {
-        attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[na].val.programmaticStreamSerializationAllowed = 1;
-        ++na;
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.numAttrs = 1;
     }
     cfg.attrs = attr;
-    cfg.numAttrs = na;
     if (cudaLaunchKernelEx(&cfg, layer_shrink_kernel, p) != cudaSuccess) return LORA_ERR_CUDA;
     note_launch(kKernLayerShrink);
     return LORA_OK;
@@ -750,6 +724,7 @@ int launch_layer_stream(const lora_table *t, const int32_t *ids, int32_t T, cons
     p.desc = t->d_desc;
     p.ids = ids;
     p.v = v;
+    p.v_parts = layer_v_parts(T, t->h);
     p.ldv = ldv;
     p.n = t->n;
     p.T = T;

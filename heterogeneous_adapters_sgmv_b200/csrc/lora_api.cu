@@ -81,6 +81,7 @@ inline int ldv_of(const lora_table *t) { return (t->max_rank + 3) & ~3; }
 
 struct WsLayout {
     size_t v, perm, seg_ptr, seg_adapter, num_segs, tile_ctr, total;
+    size_t layer, layer_total;   // lora_bgmv_layer's intermediate, behind the areas of the other calls
 };
 
 WsLayout ws_layout(const lora_table *t, int32_t T)
@@ -102,6 +103,8 @@ WsLayout ws_layout(const lora_table *t, int32_t T)
     w.tile_ctr = off + 128;   // the tcgen05 expand's tile counter, in the same 256-byte block
     off += 256;
     w.total = off;
+    w.layer = off;
+    w.layer_total = off + up256((size_t)layer_v_parts(T, t->h) * T * ldv_of(t) * sizeof(float));
     return w;
 }
 
@@ -399,7 +402,7 @@ int lora_table_info(const lora_table *t, int32_t *n, int32_t *h, int32_t *o, int
 size_t lora_workspace_bytes(const lora_table *t, int32_t T)
 {
     if (!t || T < 0) return 256;
-    return ws_layout(t, T).total;
+    return ws_layout(t, T).layer_total;
 }
 
 int lora_build_segments(const lora_table *t, const int32_t *d_ids, int32_t T, int32_t *d_perm,
@@ -652,7 +655,7 @@ int lora_bgmv_merged(const lora_table *t, const int32_t *d_ids, const float *d_w
     // with the per-token weight folded into the scale.  With room for an fp32 [T, o] sum after
     // the workspace's own areas the passes add into that sum (zeroed first) and one last launch
     // rounds y + sum once; otherwise y is rounded after each pass.
-    const size_t acc_off = (w.total + 255) / 256 * 256;
+    const size_t acc_off = (w.layer_total + 255) / 256 * 256;
     const size_t acc_bytes = (size_t)T * t->o * sizeof(float);
     float *yacc = (ws && al16(ws) && ws_bytes >= acc_off + acc_bytes)
                       ? reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + acc_off)
@@ -743,14 +746,14 @@ int lora_bgmv_layer(const lora_table *t, const int32_t *d_ids, int32_t T, const 
     if (T == 0) return LORA_OK;
     const WsLayout w = ws_layout(t, T);
     if (d_ids) {
-        if (!ws || ws_bytes < w.total) return LORA_ERR_WORKSPACE;
+        if (!ws || ws_bytes < w.layer_total) return LORA_ERR_WORKSPACE;
         if (!al16(ws)) return LORA_ERR_UNSUPPORTED;
     }
     if ((rc = check_device(t))) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     float *v = nullptr;
     if (d_ids) {
-        v = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.v);
+        v = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.layer);
         if ((rc = launch_layer_shrink(t, d_ids, T, x, ldx, v, ldv_of(t), s)) != LORA_OK) return rc;
     }
     const lora_epilogue none = {};

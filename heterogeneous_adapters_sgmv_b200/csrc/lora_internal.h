@@ -112,8 +112,11 @@ int launch_merge_finish(void *y, int64_t ldy, int32_t y_off, const float *yacc, 
 int launch_layer_gemm(const lora_table *t, const lora_segments *seg, const void *x, int64_t ldx, const void *W,
                       int64_t ldw, const lora_epilogue *epi, void *y, int64_t ldy, int32_t y_off, const void *v,
                       bool after_shrink, cudaStream_t s);
-// launch_layer_shrink: v[t, k] = s_i x[t] . A_i[k] (fp32) for per-token ids; launch_layer_stream:
-// the pass over W, with the adapter term from v when ids is not null.
+// launch_layer_shrink: v[t, k] = s_i x[t] . A_i[k] (fp32) for per-token ids, as layer_v_parts arrays of
+// [T, ldv] whose sum it is; launch_layer_stream: the pass over W, with the adapter term from v when ids
+// is not null.
+constexpr int32_t kLayerPartTokens = 512;   // batches up to this may have v in several parts
+int layer_v_parts(int32_t T, int32_t h);
 int launch_layer_shrink(const lora_table *t, const int32_t *ids, int32_t T, const void *x, int64_t ldx, float *v,
                         int32_t ldv, cudaStream_t s);
 int launch_layer_stream(const lora_table *t, const int32_t *ids, int32_t T, const void *x, int64_t ldx, const void *W,

@@ -41,7 +41,7 @@ constexpr int kShrinkThreads = kShrinkWarps * 32;     // also the tokens that a 
 constexpr int kShrinkRows = 16;                       // rank rows of a unit (mma M)
 constexpr int kShrinkTokens = 8;                      // tokens of a unit (mma N)
 constexpr int kShrinkK = 32;                          // k elements of one warp step
-constexpr int kVParts = 8;                            // parts of the k axis, at most
+constexpr int kVParts = 4;                            // parts of the k axis, at most
 
 struct LayerShrinkParams {
     const AdapterDesc *desc;
@@ -226,73 +226,110 @@ struct __align__(16) LayerStreamCtl {
     // the share its B_i and its rank (0: no adapter, -1: bad id)
 };
 
-constexpr int kLBatch = 4;                    // tokens an epilogue thread works on at a time, their loads in flight
+constexpr int kLBatch = 4;                    // tokens an epilogue thread works on at a time
 // Bytes of v that a half of the epilogue warps holds at a time: at least a batch of tokens.
 constexpr int v_bytes(int epi_warps) { return epi_warps == 8 ? 8192 : 2048; }
-static_assert(v_bytes(4) / (LORA_MAX_RANK * 4) >= kLBatch, "a batch of tokens fits");
+static_assert(v_bytes(4) / (LORA_MAX_RANK * 4) >= kLBatch && v_bytes(8) / (LORA_MAX_RANK * 4) >= 8, "a batch of tokens fits");
 
-// d[j] = sum_k B_j[n, k] v[j][k] for kLBatch tokens j; row[j] is row n of token j's B_i, v[j] its
-// intermediate (shared memory), rank[j] <= 0 for none.  Rows of a rank that is a multiple of 8 are
-// 16-byte aligned and read in 16-byte pieces, others element by element.
-__device__ __forceinline__ void expand_rows(const uint16_t *const (&row)[kLBatch], const float *const (&v)[kLBatch],
-                                            const int (&rank)[kLBatch], float (&d)[kLBatch])
-{
-    float s0[kLBatch], s1[kLBatch];
-    int even[kLBatch], odd[kLBatch], most_even = 0, most_odd = 0;
-#pragma unroll
-    for (int j = 0; j < kLBatch; ++j) {
-        s0[j] = s1[j] = 0.f;
-        even[j] = (rank[j] & 7) == 0 ? rank[j] : 0;
-        odd[j] = (rank[j] & 7) == 0 ? 0 : rank[j];
-        most_even = max(most_even, even[j]);
-        most_odd = max(most_odd, odd[j]);
+// The adapter terms of one thread's output column n, NB tokens at a time:
+//   d[j] = sum_k B_j[n, k] v_j[k].
+// Rows of a rank that is a multiple of 8 are 16-byte aligned and read NP pieces of 8 a step, the step's
+// loads together (under a saturated memory system a load takes 2 to 4 us) and the first step's before v is
+// there; other rows are read element by element, the batch's together.
+template <int NB, int NP>
+struct ExpandRows {
+    const int32_t *rank;        // per token; <= 0: none
+    const void *const *B;
+    int64_t n;
+    bool col_ok;
+    int end;                    // tokens of this thread: the batches end here
+    uint4 b[NB][NP];            // the step at hand
+
+    __device__ __forceinline__ int even(int i) const
+    {
+        const int r = i < end && col_ok ? rank[i] : 0;
+        return r > 0 && (r & 7) == 0 ? r : 0;
     }
-    for (int k = 0; k < most_even; k += 16) {
-        uint4 b[kLBatch][2];
+    __device__ __forceinline__ void load(int i, int k)
+    {
 #pragma unroll
-        for (int j = 0; j < kLBatch; ++j)
+        for (int j = 0; j < NB; ++j) {
+            const int r = even(i + j);
+            const uint16_t *row = r ? static_cast<const uint16_t *>(B[i + j]) + n * r + k : nullptr;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (k + 8 * i < even[j]) b[j][i] = *reinterpret_cast<const uint4 *>(row[j] + k + 8 * i);
-#pragma unroll
-        for (int j = 0; j < kLBatch; ++j)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (k + 8 * i < even[j]) {
-                    const float4 p = *reinterpret_cast<const float4 *>(v[j] + k + 8 * i);
-                    const float4 q = *reinterpret_cast<const float4 *>(v[j] + k + 8 * i + 4);
-                    s0[j] = fmaf(bf16_lo(b[j][i].x), p.x, s0[j]);
-                    s1[j] = fmaf(bf16_hi(b[j][i].x), p.y, s1[j]);
-                    s0[j] = fmaf(bf16_lo(b[j][i].y), p.z, s0[j]);
-                    s1[j] = fmaf(bf16_hi(b[j][i].y), p.w, s1[j]);
-                    s0[j] = fmaf(bf16_lo(b[j][i].z), q.x, s0[j]);
-                    s1[j] = fmaf(bf16_hi(b[j][i].z), q.y, s1[j]);
-                    s0[j] = fmaf(bf16_lo(b[j][i].w), q.z, s0[j]);
-                    s1[j] = fmaf(bf16_hi(b[j][i].w), q.w, s1[j]);
-                }
+            for (int e = 0; e < NP; ++e)
+                if (k + 8 * e < r) b[j][e] = *reinterpret_cast<const uint4 *>(row + 8 * e);
+        }
     }
-    for (int k = 0; k < most_odd; k += 4) {
-        uint16_t b[kLBatch][4];
+    __device__ __forceinline__ int steps(int i) const   // the batch's pieces end here; the same in all lanes
+    {
+        int most = 0;
 #pragma unroll
-        for (int j = 0; j < kLBatch; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) b[j][i] = k + i < odd[j] ? row[j][k + i] : (uint16_t)0;
-#pragma unroll
-        for (int j = 0; j < kLBatch; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (k + i < odd[j]) s0[j] = fmaf(bf16_f(b[j][i]), v[j][k + i], s0[j]);
+        for (int j = 0; j < NB; ++j) {
+            const int r = i + j < end ? rank[i + j] : 0;
+            if ((r & 7) == 0) most = max(most, r);
+        }
+        return most;
     }
+    // the batch at i, whose first step is loaded; loads the first step of the next
+    __device__ __forceinline__ void run(int i, const float *v, int ldv, float (&d)[NB])
+    {
+        const int most = steps(i);
+        for (int k = 0; k < most; k += 8 * NP) {
 #pragma unroll
-    for (int j = 0; j < kLBatch; ++j) d[j] = s0[j] + s1[j];
-}
+            for (int j = 0; j < NB; ++j) {
+                const int r = even(i + j);
+#pragma unroll
+                for (int e = 0; e < NP; ++e)
+                    if (k + 8 * e < r) {
+                        const float4 p = *reinterpret_cast<const float4 *>(v + j * ldv + k + 8 * e);
+                        const float4 q = *reinterpret_cast<const float4 *>(v + j * ldv + k + 8 * e + 4);
+                        float s0 = d[j], s1 = bf16_hi(b[j][e].x) * p.y;
+                        s0 = fmaf(bf16_lo(b[j][e].x), p.x, s0);
+                        s0 = fmaf(bf16_lo(b[j][e].y), p.z, s0);
+                        s1 = fmaf(bf16_hi(b[j][e].y), p.w, s1);
+                        s0 = fmaf(bf16_lo(b[j][e].z), q.x, s0);
+                        s1 = fmaf(bf16_hi(b[j][e].z), q.y, s1);
+                        s0 = fmaf(bf16_lo(b[j][e].w), q.z, s0);
+                        s1 = fmaf(bf16_hi(b[j][e].w), q.w, s1);
+                        d[j] = s0 + s1;
+                    }
+            }
+            if (k + 8 * NP < most) load(i, k + 8 * NP);
+        }
+        int odd[NB], longest = 0;
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            const int r = i + j < end && col_ok ? rank[i + j] : 0;
+            odd[j] = r & 7 ? r : 0;
+            longest = max(longest, odd[j]);
+        }
+        for (int k = 0; k < longest; k += 4) {
+            uint16_t w[NB][4];
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[j][e] = k + e < odd[j] ? static_cast<const uint16_t *>(B[i + j])[n * odd[j] + k + e] : (uint16_t)0;
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (k + e < odd[j]) d[j] = fmaf(bf16_f(w[j][e]), v[j * ldv + k + e], d[j]);
+        }
+        load(i + NB, 0);
+    }
+};
 
 // S CTAs of a cluster split the k axis; E epilogue warps (4 for small batches, so that three CTAs fit on
 // an SM and those of the next launch can fetch their weights while this one ends; else 8).
-template <int S, int E>
-__global__ void __launch_bounds__((2 + E) * 32, E == 4 ? 3 : 2)
+// CTAS to an SM.
+template <int S, int E, int CTAS>
+__global__ void __launch_bounds__((2 + E) * 32, CTAS)
 layer_stream_kernel(const __grid_constant__ LayerStreamParams p)
 {
+    // what the registers hold of B_i at a time: tokens and 16-byte pieces of their rows
+    constexpr int NB = kLBatch, NP = CTAS == 1 ? 4 : 2;
     constexpr int H = E / 4;   // epilogue warps per TMEM lane quarter, each with its part of the tokens
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -446,9 +483,16 @@ layer_stream_kernel(const __grid_constant__ LayerStreamParams p)
         }
         // While W streams: bias and adapter term of every output, kept in tensor memory behind the
         // accumulator.
-        if (p.early) pdl_wait();   // v
+        ExpandRows<NB, NP> ex;
+        ex.rank = tok_rank;
+        ex.B = tok_B;
+        ex.n = n;
+        ex.col_ok = col_ok;
+        ex.end = i1;
+        ex.load(i0, 0);
         float *vs = reinterpret_cast<float *>(v_buf + half * v_bytes(E));
-        const int at_once = p.ids ? v_bytes(E) / 4 / p.ldv / kLBatch * kLBatch : p.N;
+        const int at_once = p.ids ? v_bytes(E) / 4 / p.ldv / NB * NB : p.N;
+        if (p.early) pdl_wait();   // v
         for (int c = i0; c < i1; c += at_once) {
             const int ce = min(i1, c + at_once);
             if (p.ids) {
@@ -471,34 +515,29 @@ layer_stream_kernel(const __grid_constant__ LayerStreamParams p)
                 }
                 named_bar_sync(2 + half, 128);
             }
-            for (int i = c; i < ce; i += kLBatch) {
-                const uint16_t *row[kLBatch];
-                const float *v[kLBatch];
-                int r[kLBatch];
-                float d[kLBatch];
+            for (int i = c; i < ce; i += NB) {
+                float d[NB];
 #pragma unroll
-                for (int j = 0; j < kLBatch; ++j) {
-                    const bool in = i + j < ce && col_ok;
-                    r[j] = in ? tok_rank[i + j] : 0;
-                    row[j] = in ? static_cast<const uint16_t *>(tok_B[i + j]) + (int64_t)n * r[j] : nullptr;
-                    v[j] = vs + (i + j - c) * p.ldv;
-                }
-                expand_rows(row, v, r, d);
+                for (int j = 0; j < NB; ++j) d[j] = bias;
+                ex.run(i, vs + (i - c) * p.ldv, p.ldv, d);
                 __syncwarp();
-                tmem_st4(tmem_row + (uint32_t)(p.N + i), bias + d[0], bias + d[1], bias + d[2], bias + d[3]);
+#pragma unroll
+                for (int j = 0; j < NB; j += 4)
+                    if (i + j < i1) tmem_st4(tmem_row + (uint32_t)(p.N + i + j), d[j], d[j + 1], d[j + 2], d[j + 3]);
             }
         }
-        // mul and residual of a batch, one ahead of its use
-        uint16_t mu[kLBatch], re[kLBatch];
-        auto operands = [&](int i) {
+        // mul and residual of two batches, read ahead of their use
+        uint16_t mu[2][kLBatch], re[2][kLBatch];
+        auto operands = [&](int i, uint16_t (&m4)[kLBatch], uint16_t (&r4)[kLBatch]) {
 #pragma unroll
             for (int j = 0; j < kLBatch; ++j) {
                 const bool in = i + j < i1 && col_ok;
-                mu[j] = in && p.epi.mul ? p.epi.mul[(tok0 + i + j) * p.epi.ldmul + n] : (uint16_t)0;
-                re[j] = in && p.epi.res ? p.epi.res[(tok0 + i + j) * p.epi.ldres + n] : (uint16_t)0;
+                m4[j] = in && p.epi.mul ? p.epi.mul[(tok0 + i + j) * p.epi.ldmul + n] : (uint16_t)0;
+                r4[j] = in && p.epi.res ? p.epi.res[(tok0 + i + j) * p.epi.ldres + n] : (uint16_t)0;
             }
         };
-        operands(i0);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) operands(i0 + u * kLBatch, mu[u], re[u]);
         // a wait that ran out makes the warp skip the rest, but not the cluster's barriers
         bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&ctl.done), 0, p.status, p.wait_ns));
         tc_fence_after();
@@ -525,35 +564,38 @@ layer_stream_kernel(const __grid_constant__ LayerStreamParams p)
             ok = __all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&ctl.recv), 0, p.status, p.wait_ns)) && ok;
             cluster_arrive_release();   // nothing more comes to this CTA
         }
-        for (int i = i0; ok && i < i1; i += kLBatch) {
-            float z[kLBatch], f[kLBatch];
-            tmem_ld4(tmem_row + (uint32_t)(p.N + i), z);
-            tmem_ld4(tmem_row + (uint32_t)(ta + i), f);
-            float4 o[S > 1 ? S - 1 : 1];
+        for (int i2 = i0; ok && i2 < i1; i2 += 2 * kLBatch) {
 #pragma unroll
-            for (int c = 0; c < S - 1; ++c)
-                o[c] = *reinterpret_cast<const float4 *>(recv + ((c * groups + i / 4) * kLM + m) * 16);
+            for (int u = 0; u < 2; ++u) {
+                const int i = i2 + u * kLBatch;
+                if (i >= i1) break;
+                float z[kLBatch], f[kLBatch];
+                tmem_ld4(tmem_row + (uint32_t)(p.N + i), z);
+                tmem_ld4(tmem_row + (uint32_t)(ta + i), f);
+                float4 o[S > 1 ? S - 1 : 1];
 #pragma unroll
-            for (int j = 0; j < kLBatch; ++j) z[j] += f[j];
+                for (int c = 0; c < S - 1; ++c)
+                    o[c] = *reinterpret_cast<const float4 *>(recv + ((c * groups + i / 4) * kLM + m) * 16);
 #pragma unroll
-            for (int c = 0; c < S - 1; ++c) {
-                z[0] += o[c].x;
-                z[1] += o[c].y;
-                z[2] += o[c].z;
-                z[3] += o[c].w;
+                for (int j = 0; j < kLBatch; ++j) z[j] += f[j];
+#pragma unroll
+                for (int c = 0; c < S - 1; ++c) {
+                    z[0] += o[c].x;
+                    z[1] += o[c].y;
+                    z[2] += o[c].z;
+                    z[3] += o[c].w;
+                }
+                activate(z, p.epi.act);
+#pragma unroll
+                for (int j = 0; j < kLBatch; ++j) {
+                    if (p.epi.mul) z[j] *= bf16_f(mu[u][j]);
+                    if (p.epi.res) z[j] += bf16_f(re[u][j]);
+                    if (i + j < i1 && col_ok && tok_rank[i + j] >= 0)
+                        p.y[(tok0 + i + j) * p.ldy + n] = __bfloat16_as_ushort(__float2bfloat16_rn(z[j]));
+                }
+                operands(i + 2 * kLBatch, mu[u], re[u]);
+                __syncwarp();
             }
-            activate(z, p.epi.act);
-#pragma unroll
-            for (int j = 0; j < kLBatch; ++j) {
-                if (p.epi.mul) z[j] *= bf16_f(mu[j]);
-                if (p.epi.res) z[j] += bf16_f(re[j]);
-            }
-            operands(i + kLBatch);
-#pragma unroll
-            for (int j = 0; j < kLBatch; ++j)
-                if (i + j < i1 && col_ok && tok_rank[i + j] >= 0)
-                    p.y[(tok0 + i + j) * p.ldy + n] = __bfloat16_as_ushort(__float2bfloat16_rn(z[j]));
-            __syncwarp();
         }
         tc_fence_before();
     }
@@ -563,13 +605,14 @@ layer_stream_kernel(const __grid_constant__ LayerStreamParams p)
 }
 
 struct StreamShape {
-    int N, NT, S, E, stages, share, ncols, recv, alias, smem;
+    int N, NT, S, E, ctas, stages, share, ncols, recv, alias, smem;
 };
 
 // Tokens per tile: all of them up to 256 (rounded up to the MMA's 16), else equal tiles of at most
 // 256.  Clusters: as many CTAs splitting k as there is room for, up to 8.  CTAs per SM: three with four
 // epilogue warps for up to 32 tokens, two where half an SM's shared memory holds three stages and half
-// of its tensor memory the accumulator with the adapter terms behind it, else one.  One CTA alone
+// of its tensor memory the accumulator with the adapter terms behind it, else one, as where there is no
+// second CTA to put beside it.  One CTA alone
 // leaves 16 KB so that a CTA of the shrink fits beside it.
 StreamShape stream_shape(int T, int h, int o, int n_sms)
 {
@@ -582,6 +625,7 @@ StreamShape stream_shape(int T, int h, int o, int n_sms)
     const int nkb = (h + kLK - 1) / kLK;
     for (int ctas = sh.N <= 32 ? 3 : 2;; --ctas) {
         sh.E = sh.N <= 32 ? 4 : 8;
+        sh.ctas = ctas;
         const int H = sh.E / 4;
         sh.S = 1;
         while (sh.S < 8 && tiles * sh.S * 2 <= (int64_t)n_sms * std::min(ctas, 2) && sh.S * 2 <= nkb) sh.S *= 2;
@@ -592,24 +636,26 @@ StreamShape stream_shape(int T, int h, int o, int n_sms)
         const int ctl = 1024 + (int)sizeof(LayerStreamCtl) + H * v_bytes(sh.E) + sh.share * 12;
         const int recv = (sh.S - 1) * sh.share * kLM * 4;
         const int room = (ctas == 1 ? 210 : 227 / ctas - 1) * 1024 - ctl;
-        sh.alias = sh.E == 8;
+        // the peers' partial sums beside the ring where that leaves it three stages, else in it
+        sh.alias = (room - recv) / stage < 3;
         sh.stages = std::min(kLMaxStages, (room - (sh.alias ? 0 : recv)) / stage);
         if (sh.alias && sh.stages * stage < recv) sh.stages = 0;
-        if (ctas > 1 && (sh.stages < 3 || sh.ncols > 512 / ctas)) continue;
+        if (ctas > 1 && (sh.stages < 3 || sh.ncols > 512 / ctas || (sh.E == 8 && tiles * sh.S <= n_sms))) continue;
+        sh.stages = std::max(sh.alias ? (recv + stage - 1) / stage : 1, std::min(sh.stages, (nkb + sh.S - 1) / sh.S));
         sh.recv = sh.alias ? 0 : (sh.stages * stage + ctl - 1024 + 15) & ~15;
         sh.smem = sh.stages * stage + ctl + (sh.alias ? 0 : recv + 16);
         return sh;
     }
 }
 
-template <int S, int E>
+template <int S, int E, int CTAS>
 int launch_stream(const LayerStreamParams &p, const StreamShape &sh, cudaStream_t s, int dev)
 {
+    auto kern = layer_stream_kernel<S, E, CTAS>;
     static std::once_flag once[64];
     static cudaError_t attr_rc[64];
     std::call_once(once[dev], [&] {
-        attr_rc[dev] =
-            cudaFuncSetAttribute(layer_stream_kernel<S, E>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        attr_rc[dev] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     });
     if (attr_rc[dev] != cudaSuccess) return LORA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
@@ -633,19 +679,19 @@ int launch_stream(const LayerStreamParams &p, const StreamShape &sh, cudaStream_
     }
     cfg.attrs = attr;
     cfg.numAttrs = na;
-    if (cudaLaunchKernelEx(&cfg, layer_stream_kernel<S, E>, p) != cudaSuccess) return LORA_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return LORA_ERR_CUDA;
     note_launch(kKernLayerStream);
     return LORA_OK;
 }
 
-template <int E>
+template <int E, int CTAS>
 int launch_stream_width(const LayerStreamParams &p, const StreamShape &sh, cudaStream_t s, int dev)
 {
     switch (sh.S) {
-    case 8: return launch_stream<8, E>(p, sh, s, dev);
-    case 4: return launch_stream<4, E>(p, sh, s, dev);
-    case 2: return launch_stream<2, E>(p, sh, s, dev);
-    default: return launch_stream<1, E>(p, sh, s, dev);
+    case 8: return launch_stream<8, E, CTAS>(p, sh, s, dev);
+    case 4: return launch_stream<4, E, CTAS>(p, sh, s, dev);
+    case 2: return launch_stream<2, E, CTAS>(p, sh, s, dev);
+    default: return launch_stream<1, E, CTAS>(p, sh, s, dev);
     }
 }
 
@@ -743,7 +789,8 @@ int launch_layer_stream(const lora_table *t, const int32_t *ids, int32_t T, cons
     p.epi = epi_params(epi);
     p.status = t->d_status;
     p.wait_ns = wait_limit_ns();
-    return sh.E == 4 ? launch_stream_width<4>(p, sh, s, dev) : launch_stream_width<8>(p, sh, s, dev);
+    if (sh.E == 4) return launch_stream_width<4, 3>(p, sh, s, dev);
+    return sh.ctas == 2 ? launch_stream_width<8, 2>(p, sh, s, dev) : launch_stream_width<8, 1>(p, sh, s, dev);
 }
 
 }  // namespace lora

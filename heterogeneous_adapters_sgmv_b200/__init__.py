@@ -37,7 +37,7 @@ LORA_SIGMA_NONE = 0
 LORA_SIGMA_FULL = 1
 LORA_SIGMA_DIAG = 2
 LORA_MAX_MERGE = 8
-LORA_KERNEL_KINDS = 11
+LORA_KERNEL_KINDS = 12
 LORA_ACT_NONE = 0
 LORA_ACT_RELU = 1
 LORA_ACT_GELU = 2

@@ -8,10 +8,15 @@
 //
 // Bound by HBM: every operand is read once and every result written once, and between the two a
 // row stays in registers as fp32, spread over the threads of one block (so a sum over the row is a
-// shuffle and one exchange through shared memory).  The variance of a layer norm is taken from the
-// centred values in a second sum over the registers, not from the difference of two large sums.
-// h is computed from the unrounded r, so that a fused call adds no rounding of its own.
+// shuffle and one exchange through shared memory; the weights are read before the sums, which they do not
+// depend on).  Where there are many rows the blocks are
+// persistent (ring_norm_kernel): one thread brings the operands of the rows to come, the weights of each
+// row's adapter among them, into a ring in shared memory by bulk copies, and weights that serve all rows
+// once, so that no global load's latency lies between a row's sums.  The variance of a layer norm is taken from the centred values in
+// a second sum over the registers, not from the difference of two large sums.  h is computed from the
+// unrounded r, so that a fused call adds no rounding of its own.
 #include <algorithm>
+#include <mutex>
 
 #include "lora_common.cuh"
 #include "lora_internal.h"
@@ -70,23 +75,43 @@ __device__ __forceinline__ float block_sum(float v, float (*part)[32], int slot)
     return v;
 }
 
-// Thread i holds vectors i, i + NT, ... of the row (V of them at most); values past the row are 0.
+// Thread i holds vectors i, i + NT, ... of a row, V of them at most.
 template <typename E, int NT, int V>
-struct Row {
-    static constexpr int kN = Vec<E>::kN;
-    float f[V][kN];
+struct Packed {
+    uint4 w[V];
 
     __device__ __forceinline__ void load(const void *base, int64_t off, int nvec)
     {
         const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const E *>(base) + off);
-        uint4 w[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int c = threadIdx.x + j * NT;
             w[j] = c < nvec ? p[c] : make_uint4(0, 0, 0, 0);
         }
+    }
+};
+
+// The gain and shift of a norm for one row.
+template <typename E, int NT, int V>
+struct Weights {
+    Packed<E, NT, V> g, b;
+
+    __device__ __forceinline__ void load(const lora_norm &nm, int64_t wrow, int nvec)
+    {
+        if (nm.gain) g.load(nm.gain, wrow * nm.ld, nvec);
+        if (nm.shift) b.load(nm.shift, wrow * nm.ld, nvec);
+    }
+};
+
+template <typename E, int NT, int V>
+struct Row {
+    static constexpr int kN = Vec<E>::kN;
+    float f[V][kN];   // values past the row are 0
+
+    __device__ __forceinline__ void set(const Packed<E, NT, V> &p)
+    {
 #pragma unroll
-        for (int j = 0; j < V; ++j) Vec<E>::unpack(w[j], f[j]);
+        for (int j = 0; j < V; ++j) Vec<E>::unpack(p.w[j], f[j]);
     }
     __device__ __forceinline__ void store(void *base, int64_t off, int nvec) const
     {
@@ -97,8 +122,9 @@ struct Row {
             if (c < nvec) p[c] = Vec<E>::pack(f[j]);
         }
     }
-    // f <- N(f) with the weights of row `wrow`
-    __device__ __forceinline__ void normalise(const lora_norm &nm, int64_t wrow, int d, int nvec, float (*part)[32])
+    // f <- N(f)
+    __device__ __forceinline__ void normalise(const lora_norm &nm, const Weights<E, NT, V> &wt, int d, int nvec,
+                                              float (*part)[32])
     {
         const float inv_d = 1.f / (float)d;
         if (nm.kind == LORA_NORM_LAYER) {
@@ -122,23 +148,41 @@ struct Row {
         const float inv = rsqrtf(block_sum<NT>(q, part, 1) * inv_d + nm.eps);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int c = threadIdx.x + j * NT;
-            if (c >= nvec) continue;
+            if (threadIdx.x + j * NT >= nvec) continue;
             float g[kN], b[kN];
 #pragma unroll
             for (int i = 0; i < kN; ++i) {
                 g[i] = 1.f;
                 b[i] = 0.f;
             }
-            if (nm.gain) Vec<E>::unpack(reinterpret_cast<const uint4 *>(static_cast<const E *>(nm.gain) + wrow * nm.ld)[c], g);
-            if (nm.shift)
-                Vec<E>::unpack(reinterpret_cast<const uint4 *>(static_cast<const E *>(nm.shift) + wrow * nm.ld)[c], b);
+            if (nm.gain) Vec<E>::unpack(wt.g.w[j], g);
+            if (nm.shift) Vec<E>::unpack(wt.b.w[j], b);
 #pragma unroll
             for (int i = 0; i < kN; ++i) f[j][i] = fmaf(f[j][i] * inv, g[i], b[i]);
         }
     }
 };
 
+// u * gate * branch_scale + res_scale * residual
+template <typename E>
+__device__ __forceinline__ void join(const lora_residual &rs, float (&f)[Vec<E>::kN], const uint4 &gate, const uint4 &res)
+{
+    float o[Vec<E>::kN];
+    if (rs.gate_kind != LORA_GATE_NONE) {
+        Vec<E>::unpack(gate, o);
+#pragma unroll
+        for (int i = 0; i < Vec<E>::kN; ++i) f[i] *= o[i];
+    }
+#pragma unroll
+    for (int i = 0; i < Vec<E>::kN; ++i) f[i] *= rs.branch_scale;
+    if (rs.residual) {
+        Vec<E>::unpack(res, o);
+#pragma unroll
+        for (int i = 0; i < Vec<E>::kN; ++i) f[i] = fmaf(rs.res_scale, o[i], f[i]);
+    }
+}
+
+// One row a block.
 template <typename E, int NT, int V, bool AFTER>
 __global__ void __launch_bounds__(NT) block_norm_kernel(const __grid_constant__ NormParams p)
 {
@@ -147,8 +191,12 @@ __global__ void __launch_bounds__(NT) block_norm_kernel(const __grid_constant__ 
     pdl_launch_dependents();
     const int64_t t = blockIdx.x;
     const int nvec = p.d / Vec<E>::kN;
-    Row<E, NT, V> x;
+    Packed<E, NT, V> x, res, gate;
     x.load(p.x, t * p.ldx, nvec);
+    if constexpr (AFTER) {
+        if (p.res.residual) res.load(p.res.residual, t * p.res.ldres, nvec);
+        if (p.res.gate_kind == LORA_GATE_TOKEN) gate.load(p.res.gate, t * p.res.ldgate, nvec);
+    }
     int id = -1;
     if (p.ids) {
         id = p.ids[t];
@@ -157,76 +205,293 @@ __global__ void __launch_bounds__(NT) block_norm_kernel(const __grid_constant__ 
             return;
         }
     }
-    const int64_t wrow = id + 1;
+    const int64_t wrow = (int64_t)id + 1;
+    Weights<E, NT, V> w1, w2;
+    if (p.norm.kind) w1.load(p.norm, wrow, nvec);
+    if constexpr (AFTER) {
+        if (p.res.gate_kind == LORA_GATE_ADAPTER) gate.load(p.res.gate, wrow * p.res.ldgate, nvec);
+        if (p.h) w2.load(p.next, wrow, nvec);
+    }
+    Row<E, NT, V> f;
+    f.set(x);
+    if (p.norm.kind) f.normalise(p.norm, w1, p.d, nvec, part);
     if constexpr (!AFTER) {
-        x.normalise(p.norm, wrow, p.d, nvec, part);
-        x.store(p.h, t * p.ldh, nvec);
+        f.store(p.h, t * p.ldh, nvec);
     } else {
-        Row<E, NT, V> s;
-        if (p.res.residual) {
-            s.load(p.res.residual, t * p.res.ldres, nvec);
-        } else {
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-#pragma unroll
-                for (int i = 0; i < Vec<E>::kN; ++i) s.f[j][i] = 0.f;
-        }
-        if (p.norm.kind) x.normalise(p.norm, wrow, p.d, nvec, part);
-        if (p.res.gate_kind != LORA_GATE_NONE) {
-            Row<E, NT, V> g;
-            g.load(p.res.gate, (p.res.gate_kind == LORA_GATE_TOKEN ? t : wrow) * p.res.ldgate, nvec);
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-#pragma unroll
-                for (int i = 0; i < Vec<E>::kN; ++i) x.f[j][i] *= g.f[j][i];
-        }
-        const float a = p.res.residual ? p.res.res_scale : 0.f, c = p.res.branch_scale;
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-#pragma unroll
-            for (int i = 0; i < Vec<E>::kN; ++i) x.f[j][i] = fmaf(a, s.f[j][i], c * x.f[j][i]);
-        if (p.r) x.store(p.r, t * p.ldr, nvec);
+        for (int j = 0; j < V; ++j) join<E>(p.res, f.f[j], gate.w[j], res.w[j]);
+        if (p.r) f.store(p.r, t * p.ldr, nvec);
         if (p.h) {
-            // the first norm's sums are read by every thread before the second norm's are written
-            if (NT > 32 && p.norm.kind) __syncthreads();
-            x.normalise(p.next, wrow, p.d, nvec, part);
-            x.store(p.h, t * p.ldh, nvec);
+            if (NT > 32 && p.norm.kind) __syncthreads();   // the first norm's sums are read by all
+            f.normalise(p.next, w2, p.d, nvec, part);
+            f.store(p.h, t * p.ldh, nvec);
         }
     }
 }
 
-template <typename E, int NT, int V>
-int launch_one(const NormParams &p, bool after, cudaStream_t s)
+// ------------------------------------------------------------------------------- persistent blocks
+
+// The seven operands a row may have, in the order in which they lie in a stage (or in the block's area for
+// what serves all rows).
+enum NormOperand { kOpX, kOpRes, kOpGate, kOpGain1, kOpShift1, kOpGain2, kOpShift2, kOps };
+constexpr int kNormStages = 4;
+// Blocks per SM: half its threads, or a quarter for the registers of the larger kernel.
+constexpr int ring_blocks(int nt, bool after) { return nt >= (after ? 512 : 1024) ? 1 : (after ? 768 : 1024) / nt; }
+
+struct RingShape {
+    int32_t row_bytes, stages, stage_bytes;
+    int32_t fixed_bytes;          // of the operands that serve all rows, at the start of shared memory
+    int32_t at[kOps];             // offset of each operand in its stage or area, -1: absent
+    int32_t per_row;              // bit: the operand changes from row to row
+    uint64_t wait_ns;
+};
+
+template <typename E, int NT, int V, bool AFTER>
+__global__ void __launch_bounds__(NT, ring_blocks(NT, AFTER))
+ring_norm_kernel(const __grid_constant__ NormParams p, const __grid_constant__ RingShape sh)
+{
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float part[2][32];
+    __shared__ uint64_t full[kNormStages], fixed;
+    __shared__ int32_t row_id[kNormStages];
+    uint8_t *ring = smem + sh.fixed_bytes;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < sh.stages; ++i) mbar_init(smem_u32(&full[i]), 1);
+        mbar_init(smem_u32(&fixed), 1);
+        fence_mbar_init_cluster();
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+    const int nvec = p.d / Vec<E>::kN;
+    // Row `t` of operand `op` for a token with adapter row `w`.
+    auto source = [&](int op, int64_t t, int64_t w) -> const void * {
+        const E *b;
+        int64_t row;
+        switch (op) {
+        case kOpX: b = static_cast<const E *>(p.x), row = t * p.ldx; break;
+        case kOpRes: b = static_cast<const E *>(p.res.residual), row = t * p.res.ldres; break;
+        case kOpGate:
+            b = static_cast<const E *>(p.res.gate);
+            row = (p.res.gate_kind == LORA_GATE_TOKEN ? t : w) * p.res.ldgate;
+            break;
+        case kOpGain1: b = static_cast<const E *>(p.norm.gain), row = w * p.norm.ld; break;
+        case kOpShift1: b = static_cast<const E *>(p.norm.shift), row = w * p.norm.ld; break;
+        case kOpGain2: b = static_cast<const E *>(p.next.gain), row = w * p.next.ld; break;
+        default: b = static_cast<const E *>(p.next.shift), row = w * p.next.ld; break;
+        }
+        return b + row;
+    };
+    // Thread 0: the operands of row t, whose adapter is `id`, into stage s.
+    auto fetch = [&](int64_t t, int s, int id) {
+        const bool bad = id < -1 || id >= p.n;   // nothing is read for it: the row stays as it was
+        const uint32_t bar = smem_u32(&full[s]);
+        row_id[s] = bad ? -2 : id;
+        mbar_arrive_expect_tx(bar, bad ? 0u : (uint32_t)sh.stage_bytes);
+        if (bad) return;
+#pragma unroll
+        for (int op = 0; op < kOps; ++op)
+            if ((sh.per_row >> op) & 1)
+                bulk_g2s(smem_u32(ring) + (uint32_t)(s * sh.stage_bytes + sh.at[op]), source(op, t, (int64_t)id + 1),
+                         (uint32_t)sh.row_bytes, bar);
+    };
+    int ahead = -1;   // thread 0: adapter of the next row to fetch
+    if (threadIdx.x == 0) {
+        mbar_arrive_expect_tx(smem_u32(&fixed), (uint32_t)sh.fixed_bytes);
+#pragma unroll
+        for (int op = 0; op < kOps; ++op)
+            if (sh.at[op] >= 0 && !((sh.per_row >> op) & 1))
+                bulk_g2s(smem_u32(smem) + (uint32_t)sh.at[op], source(op, 0, 0), (uint32_t)sh.row_bytes, smem_u32(&fixed));
+        int ids[kNormStages + 1];
+#pragma unroll
+        for (int i = 0; i <= kNormStages; ++i) {
+            const int64_t t = blockIdx.x + (int64_t)i * gridDim.x;
+            ids[i] = p.ids && i <= sh.stages && t < p.T ? p.ids[t] : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < kNormStages; ++i) {
+            const int64_t t = blockIdx.x + (int64_t)i * gridDim.x;
+            if (i < sh.stages && t < p.T) fetch(t, i, ids[i]);
+            if (i < sh.stages) ahead = ids[i + 1];
+        }
+    }
+    __syncthreads();
+    bool ok = mbar_wait(smem_u32(&fixed), 0, p.status, sh.wait_ns);
+    int s = 0;
+    uint32_t phase = 0;
+    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+        const int64_t behind = t + (int64_t)sh.stages * gridDim.x;   // the row that takes this stage next
+        ok = mbar_wait(smem_u32(&full[s]), phase, p.status, sh.wait_ns) && ok;
+        auto operand = [&](int op) {
+            return reinterpret_cast<const uint4 *>(((sh.per_row >> op) & 1 ? ring + s * sh.stage_bytes : smem) + sh.at[op]);
+        };
+        auto weights = [&](const lora_norm &nm, int gain, Weights<E, NT, V> &w) {
+            if (nm.gain) w.g.load(operand(gain), 0, nvec);
+            if (nm.shift) w.b.load(operand(gain + 1), 0, nvec);
+        };
+        const bool bad = row_id[s] == -2;
+        if (bad && ok) {
+            if (threadIdx.x == 0) atomicOr(p.status, LORA_STATUS_BAD_ID);
+        } else if (ok) {
+            Packed<E, NT, V> in;
+            Row<E, NT, V> f;
+            Weights<E, NT, V> w;
+            in.load(operand(kOpX), 0, nvec);
+            f.set(in);
+            if (p.norm.kind) {
+                weights(p.norm, kOpGain1, w);
+                f.normalise(p.norm, w, p.d, nvec, part);
+            }
+            if constexpr (!AFTER) {
+                f.store(p.h, t * p.ldh, nvec);
+            } else {
+                Packed<E, NT, V> gate;
+                if (p.res.residual) in.load(operand(kOpRes), 0, nvec);
+                if (p.res.gate_kind != LORA_GATE_NONE) gate.load(operand(kOpGate), 0, nvec);
+#pragma unroll
+                for (int j = 0; j < V; ++j) join<E>(p.res, f.f[j], gate.w[j], in.w[j]);
+                if (p.r) f.store(p.r, t * p.ldr, nvec);
+                if (p.h) {
+                    if (NT > 32 && p.norm.kind) __syncthreads();   // the first norm's sums are read by all
+                    weights(p.next, kOpGain2, w);
+                    f.normalise(p.next, w, p.d, nvec, part);
+                    f.store(p.h, t * p.ldh, nvec);
+                }
+            }
+        }
+        // The stage and the sums have been read by all.  A wait that ran out anywhere ends the block, once
+        // its copies have landed.
+        if (!__syncthreads_and(ok)) {
+            if (threadIdx.x == 0)
+                for (int i = 0; i < sh.stages; ++i) {
+                    if (t + (int64_t)i * gridDim.x < p.T) mbar_wait(smem_u32(&full[s]), phase, p.status, sh.wait_ns);
+                    if (++s == sh.stages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                }
+            return;
+        }
+        if (threadIdx.x == 0 && behind < p.T) {
+            fetch(behind, s, ahead);
+            if (p.ids && behind + gridDim.x < p.T) ahead = p.ids[behind + gridDim.x];
+        }
+        if (++s == sh.stages) {
+            s = 0;
+            phase ^= 1;
+        }
+    }
+}
+
+cudaLaunchConfig_t norm_config(int64_t grid, int block, size_t smem, cudaStream_t s, cudaLaunchAttribute *attr)
 {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.T);
-    cfg.blockDim = dim3(NT);
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cfg.attrs = attr;
     if (options().pdl) {
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.numAttrs = 1;
     }
-    cfg.attrs = attr;
-    const cudaError_t e = after ? cudaLaunchKernelEx(&cfg, block_norm_kernel<E, NT, V, true>, p)
-                                : cudaLaunchKernelEx(&cfg, block_norm_kernel<E, NT, V, false>, p);
-    if (e != cudaSuccess) return LORA_ERR_CUDA;
+    return cfg;
+}
+
+// Launches the persistent kernel, or returns LORA_ERR_UNSUPPORTED where two stages do not fit.
+template <typename E, int NT, int V, bool AFTER>
+int launch_ring(const NormParams &p, int dev, int sms, cudaStream_t s)
+{
+    auto kern = ring_norm_kernel<E, NT, V, AFTER>;
+    constexpr int kShared = 227 * 1024;
+    RingShape sh = {};
+    sh.row_bytes = p.d * (int)sizeof(E);
+    sh.wait_ns = wait_limit_ns();
+    const bool gate = AFTER && p.res.gate_kind != LORA_GATE_NONE;
+    const bool present[kOps] = {true,
+                                AFTER && p.res.residual,
+                                gate,
+                                p.norm.kind && p.norm.gain,
+                                p.norm.kind && p.norm.shift,
+                                AFTER && p.next.kind && p.next.gain,
+                                AFTER && p.next.kind && p.next.shift};
+    const bool rows[kOps] = {true,
+                             true,
+                             p.res.gate_kind == LORA_GATE_TOKEN || (p.ids && p.res.ldgate),
+                             p.ids && p.norm.ld,
+                             p.ids && p.norm.ld,
+                             p.ids && p.next.ld,
+                             p.ids && p.next.ld};
+    for (int op = 0; op < kOps; ++op) {
+        int32_t &bytes = rows[op] ? sh.stage_bytes : sh.fixed_bytes;
+        sh.at[op] = present[op] ? bytes : -1;
+        if (!present[op]) continue;
+        bytes += sh.row_bytes;
+        if (rows[op]) sh.per_row |= 1 << op;
+    }
+    // As many blocks as registers allow, as long as each has a ring of at least two stages.
+    int blocks = ring_blocks(NT, AFTER);
+    auto depth = [&](int n) { return (kShared / n - 2048 - sh.fixed_bytes) / sh.stage_bytes; };
+    while (blocks > 1 && depth(blocks) < 2) --blocks;
+    sh.stages = std::min(kNormStages, depth(blocks));
+    if (sh.stages < 2) return LORA_ERR_UNSUPPORTED;
+    static std::once_flag once[64];
+    static cudaError_t attr_rc[64];
+    std::call_once(once[dev], [&] {
+        attr_rc[dev] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared - 1024);
+    });
+    if (attr_rc[dev] != cudaSuccess) return LORA_ERR_CUDA;
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = norm_config(std::min<int64_t>(p.T, (int64_t)blocks * sms), NT,
+                                               (size_t)(sh.fixed_bytes + sh.stages * sh.stage_bytes), s, attr);
+    if (cudaLaunchKernelEx(&cfg, kern, p, sh) != cudaSuccess) return LORA_ERR_CUDA;
+    note_launch(kKernRingNorm);
+    return LORA_OK;
+}
+
+template <typename E, int NT, int V, bool AFTER>
+int launch_kernel(const NormParams &p, cudaStream_t s)
+{
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = norm_config(p.T, NT, 0, s, attr);
+    if (cudaLaunchKernelEx(&cfg, block_norm_kernel<E, NT, V, AFTER>, p) != cudaSuccess) return LORA_ERR_CUDA;
     note_launch(kKernBlockNorm);
     return LORA_OK;
+}
+
+// Rows for every block to run several times are worth a ring.
+constexpr int kRingRowsPerSm = 12;
+
+// NT threads with V vectors each for a row: NT1, V1 where a block takes one row (latency counts, so many
+// threads), NT2, V2 for persistent blocks (rows side by side count, so few; but not more than two vectors a
+// thread, whose registers spill otherwise).
+template <typename E, int NT1, int V1, int NT2, int V2>
+int launch_one(const NormParams &p, bool after, int dev, int sms, cudaStream_t s)
+{
+    if (p.T >= kRingRowsPerSm * sms) {
+        const int rc = after ? launch_ring<E, NT2, V2, true>(p, dev, sms, s) : launch_ring<E, NT2, V2, false>(p, dev, sms, s);
+        if (rc != LORA_ERR_UNSUPPORTED) return rc;
+    }
+    return after ? launch_kernel<E, NT1, V1, true>(p, s) : launch_kernel<E, NT1, V1, false>(p, s);
 }
 
 template <typename E>
 int launch_typed(const NormParams &p, bool after, cudaStream_t s)
 {
     const int nvec = p.d / Vec<E>::kN;
-    if (nvec <= 32) return launch_one<E, 32, 1>(p, after, s);
-    if (nvec <= 128) return launch_one<E, 128, 1>(p, after, s);
-    if (nvec <= 256) return launch_one<E, 256, 1>(p, after, s);
-    if (nvec <= 512) return launch_one<E, 256, 2>(p, after, s);
-    if (nvec <= 1024) return launch_one<E, 512, 2>(p, after, s);
-    if (nvec <= 2048) return launch_one<E, 512, 4>(p, after, s);
-    if constexpr (LORA_MAX_NORM_WIDTH > 2048 * Vec<E>::kN) return launch_one<E, 1024, 4>(p, after, s);
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return LORA_ERR_CUDA;
+    static std::once_flag once[64];
+    static int sms[64];
+    std::call_once(once[dev], [&] { cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev); });
+    if (sms[dev] < 1) return LORA_ERR_CUDA;
+    if (nvec <= 32) return launch_one<E, 32, 1, 32, 1>(p, after, dev, sms[dev], s);
+    if (nvec <= 128) return launch_one<E, 128, 1, 64, 2>(p, after, dev, sms[dev], s);
+    if (nvec <= 256) return launch_one<E, 256, 1, 128, 2>(p, after, dev, sms[dev], s);
+    if (nvec <= 512) return launch_one<E, 256, 2, 256, 2>(p, after, dev, sms[dev], s);
+    if (nvec <= 1024) return launch_one<E, 512, 2, 512, 2>(p, after, dev, sms[dev], s);
+    if (nvec <= 2048) return launch_one<E, 512, 4, 1024, 2>(p, after, dev, sms[dev], s);
+    if constexpr (LORA_MAX_NORM_WIDTH > 2048 * Vec<E>::kN) return launch_one<E, 1024, 4, 1024, 4>(p, after, dev, sms[dev], s);
     return LORA_ERR_UNSUPPORTED;
 }
 static_assert(LORA_MAX_NORM_WIDTH <= 1024 * 4 * Vec<float>::kN && LORA_MAX_NORM_WIDTH <= 2048 * Vec<__nv_bfloat16>::kN,

@@ -25,7 +25,7 @@ static std::atomic<int64_t> g_launches[kKernKinds];
 static const char *const kKernelNames[kKernKinds] = {
     "lora_decode_kernel", "count_segments_kernel", "build_segments_kernel", "prefill_shrink_kernel",
     "prefill_expand_kernel", "base_gemm_kernel", "merge_finish_kernel", "layer_shrink_kernel", "layer_stream_kernel",
-    "layer_gemm_kernel", "block_norm_kernel",
+    "layer_gemm_kernel", "block_norm_kernel", "ring_norm_kernel",
 };
 
 void note_launch(KernelKind k) { g_launches[k].fetch_add(1, std::memory_order_relaxed); }

@@ -82,7 +82,8 @@ Options &options();
 // Host-side count of accepted launches per kernel (lora_kernel_launches).
 enum KernelKind {
     kKernDecode = 0, kKernCountSegments, kKernBuildSegments, kKernPrefillShrink, kKernPrefillExpand,
-    kKernBaseGemm, kKernMergeFinish, kKernLayerShrink, kKernLayerStream, kKernLayerGemm, kKernBlockNorm, kKernKinds
+    kKernBaseGemm, kKernMergeFinish, kKernLayerShrink, kKernLayerStream, kKernLayerGemm, kKernBlockNorm,
+    kKernRingNorm, kKernKinds
 };
 void note_launch(KernelKind k);
 

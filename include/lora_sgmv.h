@@ -399,11 +399,11 @@ int lora_get_option(const char *key, int64_t *value);
  * LORA_KERNEL_KINDS - 1 (0 the decode kernel, 1 and 2 the two segment-building kernels, 3 and
  * 4 the tcgen05 shrink and expand, 5 the fused base GEMM, 6 the merged ensembles' final
  * rounding, 7 and 8 the shrink and the weight pass of lora_bgmv_layer, 9 the product of
- * lora_sgmv_layer, 10 the norms).  lora_kernel_name returns the kernel's name (static text; NULL outside that range) and lora_kernel_launches its count (-1
+ * lora_sgmv_layer, 10 and 11 the norms).  lora_kernel_name returns the kernel's name (static text; NULL outside that range) and lora_kernel_launches its count (-1
  * outside that range).  A count says that a launch was enqueued, not that it has finished;
  * lora_get_status reports what the device found.  Tests read them to see which path a call
  * took. */
-#define LORA_KERNEL_KINDS 11
+#define LORA_KERNEL_KINDS 12
 const char *lora_kernel_name(int32_t kind);
 int64_t lora_kernel_launches(int32_t kind);
 

@@ -82,6 +82,22 @@ __device__ __forceinline__ int nth_member(const uint32_t *members, int nth, int 
     return tok;
 }
 
+// Asks L2 for the rows of A_i of the batch's first 256 tokens: a few blocks share each token (the first of
+// those with its adapter).
+__device__ __forceinline__ void shrink_hints(const LayerShrinkParams &p)
+{
+    const volatile int32_t *ids = p.ids;
+    const int tid = threadIdx.x, tokens = min(p.T, kShrinkThreads);
+    const int blocks = max(1, (int)gridDim.x / tokens), t = blockIdx.x / blocks;
+    const int mine = tid < tokens ? ids[tid] : -1, a = t < tokens ? ids[t] : -1;
+    if (__syncthreads_or(tid < t && mine == a) || a < 0 || a >= p.n) return;
+    const AdapterDesc d = p.desc[a];
+    const int64_t bytes = (int64_t)d.rank * p.h * 2;
+    for (int64_t at = ((int64_t)(blockIdx.x % blocks) * kShrinkThreads + tid) * 128; at < bytes;
+         at += (int64_t)blocks * kShrinkThreads * 128)
+        prefetch_l2(static_cast<const uint8_t *>(d.A) + at);
+}
+
 // A unit of work is up to 8 tokens of one adapter (found among 256 consecutive tokens) times 16 of its
 // rank rows times one part of the k axis, so a row of A_i is read once for 8 tokens and x once for 16
 // rows.  The reads bound it; the products (2 T r h flop, a few percent of the pass over W) go to the
@@ -98,8 +114,11 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) layer_shrink_kernel(const _
     __shared__ int32_t warp_units[kShrinkWarps];
     __shared__ uint32_t members[kShrinkWarps];
     __shared__ float part[kShrinkWarps][kShrinkRows * kShrinkTokens];
-    // the wait comes first: launch_dependents then tells the pass over W that x and the epilogue's
-    // operands are final, and that only v is still to come
+    // While the kernel before ends, the weights that this batch will ask for go to L2.  The ids may not be
+    // final yet: what is read here serves as a hint and for nothing else (a range check makes any value safe).
+    shrink_hints(p);
+    // then the wait, and only behind it launch_dependents, which tells the pass over W that x and the
+    // epilogue's operands are final and that only v is still to come
     pdl_wait();
     pdl_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;

@@ -65,21 +65,26 @@ __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Token of the nth set bit of the window's mask, counting from 0; -1 when there are not that many.
+// Token of the nth (0 to 7) set bit of the window's mask; -1 when there are not that many.
 __device__ __forceinline__ int nth_member(const uint32_t *members, int nth, int w0)
 {
-    int tok = -1;
+    uint32_t word = 0;
+    int base = -1;
 #pragma unroll
     for (int i = 0; i < kShrinkWarps; ++i) {
-        uint32_t m = members[i];
+        const uint32_t m = members[i];
         const int c = __popc(m);
-        if (tok < 0 && nth < c) {
-            for (int k = 0; k < nth; ++k) m &= m - 1;
-            tok = w0 + 32 * i + __ffs(m) - 1;
+        if (base < 0 && nth < c) {
+            word = m;
+            base = w0 + 32 * i;
         }
-        nth -= c;
+        if (base < 0) nth -= c;
     }
-    return tok;
+    if (base < 0) return -1;
+#pragma unroll
+    for (int k = 0; k < kShrinkTokens - 1; ++k)
+        if (k < nth) word &= word - 1;
+    return base + __ffs(word) - 1;
 }
 
 // Asks L2 for the rows of A_i of the batch's first 256 tokens: a few blocks share each token (the first of
@@ -163,7 +168,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) layer_shrink_kernel(const _
         first_unit[tid] = first;
         // ---- every gridDim.x-th item
         for (; item - skipped < (int64_t)total * p.parts; item += gridDim.x) {
-            const int u = (int)((item - skipped) / p.parts), ks = (int)((item - skipped) % p.parts);
+            const int at_item = (int)(item - skipped), u = at_item / p.parts, ks = at_item - u * p.parts;
             const int lo = __syncthreads_count(first <= u) - 1;   // the token that leads the unit
             const int ad = ids[lo], k0 = (u - first_unit[lo]) * kShrinkRows;
             const uint32_t vote = __ballot_sync(0xffffffffu, tid >= lo && a == ad);
@@ -175,10 +180,10 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) layer_shrink_kernel(const _
             const uint16_t *a0 = k0 + row < rank ? A + (int64_t)(k0 + row) * p.h + kl : nullptr;
             const uint16_t *a1 = k0 + row + 8 < rank ? A + (int64_t)(k0 + row + 8) * p.h + kl : nullptr;
             const uint16_t *xr = tok >= 0 ? p.x + tok * p.ldx + kl : nullptr;
-            const int s1 = (int)((int64_t)(ks + 1) * steps / p.parts);
+            const int per = (steps + p.parts - 1) / p.parts, s1 = min(steps, (ks + 1) * per);
             float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-            for (int j = (int)((int64_t)ks * steps / p.parts) + warp; j < s1; j += kShrinkWarps) {
+            for (int j = ks * per + warp; j < s1; j += kShrinkWarps) {
                 const int k = j * kShrinkK;
                 const bool in = k + kl < p.h;   // h is a multiple of 8
                 const uint4 zero = make_uint4(0, 0, 0, 0);

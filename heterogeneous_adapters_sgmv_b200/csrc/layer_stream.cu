@@ -345,15 +345,14 @@ struct ExpandRows {
     }
 };
 
-// S CTAs of a cluster split the k axis; E epilogue warps (4 for small batches, so that three CTAs fit on
-// an SM and those of the next launch can fetch their weights while this one ends; else 8).
-// CTAS to an SM.
+// S CTAs of a cluster split the k axis; E epilogue warps (4 for small batches, which have few outputs, else
+// 8); CTAS to an SM.
 template <int S, int E, int CTAS>
 __global__ void __launch_bounds__((2 + E) * 32, CTAS)
 layer_stream_kernel(const __grid_constant__ LayerStreamParams p)
 {
     // what the registers hold of B_i at a time: tokens and 16-byte pieces of their rows
-    constexpr int NB = kLBatch, NP = CTAS == 1 ? 4 : 2;
+    constexpr int NB = kLBatch, NP = E == 4 || CTAS == 1 ? 4 : 2;
     constexpr int H = E / 4;   // epilogue warps per TMEM lane quarter, each with its part of the tokens
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -633,12 +632,13 @@ struct StreamShape {
 };
 
 // Tokens per tile: all of them up to 256 (rounded up to the MMA's 16), else equal tiles of at most
-// 256.  Clusters: as many CTAs splitting k as there is room for, up to 8.  CTAs per SM: three with four
-// epilogue warps for up to 32 tokens, two where half an SM's shared memory holds three stages and half
-// of its tensor memory the accumulator with the adapter terms behind it, else one, as where there is no
-// second CTA to put beside it.  One CTA alone
+// 256.  Clusters: up to 8 CTAs split k, without adapters as many as fit two to an SM (4096 -> 4096, one token:
+// 8.3 us with 8, 9.3 with 4), with adapters no more than make four CTAs for five SMs (64 tokens: 17.5 us with 4,
+// 18.9 with 8; 14336 outputs: 32.0 with 2, 36.4 with 1), since every CTA more waits for v and for its peers.
+// CTAs per SM: two where half an SM's shared memory holds three stages and half of its tensor memory the
+// accumulator with the adapter terms behind it, else one, as where there is no second CTA to put beside it.  One CTA alone
 // leaves 16 KB so that a CTA of the shrink fits beside it.
-StreamShape stream_shape(int T, int h, int o, int n_sms)
+StreamShape stream_shape(int T, int h, int o, int n_sms, bool adapters)
 {
     StreamShape sh;
     sh.NT = (T + kLMaxN - 1) / kLMaxN;
@@ -647,12 +647,14 @@ StreamShape stream_shape(int T, int h, int o, int n_sms)
     const int stage = kLWBytes + sh.N * 128;
     const int64_t tiles = (int64_t)((o + kLM - 1) / kLM) * sh.NT;
     const int nkb = (h + kLK - 1) / kLK;
-    for (int ctas = sh.N <= 32 ? 3 : 2;; --ctas) {
+    for (int ctas = 2;; --ctas) {
         sh.E = sh.N <= 32 ? 4 : 8;
         sh.ctas = ctas;
         const int H = sh.E / 4;
         sh.S = 1;
-        while (sh.S < 8 && tiles * sh.S * 2 <= (int64_t)n_sms * std::min(ctas, 2) && sh.S * 2 <= nkb) sh.S *= 2;
+        while (sh.S < 8 && tiles * sh.S * 2 <= (int64_t)n_sms * ctas && sh.S * 2 <= nkb &&
+               !(adapters && tiles * sh.S * 5 >= 4ll * n_sms))
+            sh.S *= 2;
         sh.share = ((std::min(sh.N, per) + sh.S - 1) / sh.S + kLBatch - 1) / kLBatch * kLBatch;
         const int hs = (sh.share / H + kLBatch - 1) / kLBatch * kLBatch;
         sh.ncols = 32;
@@ -664,7 +666,7 @@ StreamShape stream_shape(int T, int h, int o, int n_sms)
         sh.alias = (room - recv) / stage < 3;
         sh.stages = std::min(kLMaxStages, (room - (sh.alias ? 0 : recv)) / stage);
         if (sh.alias && sh.stages * stage < recv) sh.stages = 0;
-        if (ctas > 1 && (sh.stages < 3 || sh.ncols > 512 / ctas || (sh.E == 8 && tiles * sh.S <= n_sms))) continue;
+        if (ctas > 1 && (sh.stages < 3 || sh.ncols > 512 / ctas || tiles * sh.S <= n_sms)) continue;
         sh.stages = std::max(sh.alias ? (recv + stage - 1) / stage : 1, std::min(sh.stages, (nkb + sh.S - 1) / sh.S));
         sh.recv = sh.alias ? 0 : (sh.stages * stage + ctl - 1024 + 15) & ~15;
         sh.smem = sh.stages * stage + ctl + (sh.alias ? 0 : recv + 16);
@@ -785,7 +787,7 @@ int launch_layer_stream(const lora_table *t, const int32_t *ids, int32_t T, cons
 {
     int dev = 0, n_sms = 0, rc;
     if (device_sms(&dev, &n_sms) != LORA_OK) return LORA_ERR_CUDA;
-    const StreamShape sh = stream_shape(T, t->h, t->o, n_sms);
+    const StreamShape sh = stream_shape(T, t->h, t->o, n_sms, ids != nullptr);
     LayerStreamParams p;
     std::memset(&p, 0, sizeof p);
     if ((rc = encode_sw128(&p.tm_x, x, (uint64_t)t->h, (uint64_t)T, (uint64_t)ldx, (uint32_t)sh.N)) != LORA_OK ||
@@ -813,7 +815,7 @@ int launch_layer_stream(const lora_table *t, const int32_t *ids, int32_t T, cons
     p.epi = epi_params(epi);
     p.status = t->d_status;
     p.wait_ns = wait_limit_ns();
-    if (sh.E == 4) return launch_stream_width<4, 3>(p, sh, s, dev);
+    if (sh.E == 4) return sh.ctas == 2 ? launch_stream_width<4, 2>(p, sh, s, dev) : launch_stream_width<4, 1>(p, sh, s, dev);
     return sh.ctas == 2 ? launch_stream_width<8, 2>(p, sh, s, dev) : launch_stream_width<8, 1>(p, sh, s, dev);
 }
 

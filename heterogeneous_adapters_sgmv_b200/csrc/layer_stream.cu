@@ -655,7 +655,8 @@ StreamShape stream_shape(int T, int h, int o, int n_sms, bool adapters)
         while (sh.S < 8 && tiles * sh.S * 2 <= (int64_t)n_sms * ctas && sh.S * 2 <= nkb &&
                !(adapters && tiles * sh.S * 5 >= 4ll * n_sms))
             sh.S *= 2;
-        sh.share = ((std::min(sh.N, per) + sh.S - 1) / sh.S + kLBatch - 1) / kLBatch * kLBatch;
+        // S shares cover a whole tile (N, which is more than `per` when there are several)
+        sh.share = ((std::min(sh.N, T) + sh.S - 1) / sh.S + kLBatch - 1) / kLBatch * kLBatch;
         const int hs = (sh.share / H + kLBatch - 1) / kLBatch * kLBatch;
         sh.ncols = 32;
         while (sh.ncols < sh.N + H * hs) sh.ncols *= 2;

@@ -129,7 +129,10 @@ class Layer:
 # few W tiles and a long k axis split k over 8 CTAs, a short one over none
 @pytest.mark.parametrize("T,h,o", [(1, 8, 8), (1, 4096, 8), (2, 64, 128), (15, 72, 136), (16, 512, 128),
                                    (17, 1000, 264), (33, 200, 1032), (64, 1096, 1000), (130, 128, 520),
-                                   (177, 320, 256), (256, 640, 128), (257, 328, 392), (515, 256, 144)])
+                                   (177, 320, 256), (256, 640, 128), (257, 328, 392), (515, 256, 144),
+                                   # several token tiles, whose rounded-up size the shares of a cluster of 2, 4
+                                   # and 8 have to cover
+                                   (260, 128, 264), (261, 304, 136), (777, 128, 64), (521, 520, 72), (389, 192, 72)])
 def test_bgmv_layer_sizes(T, h, o):
     m = Layer(T, h, o, (16, 3, 128, 8, 20), seed=1, bias=True, act="silu", mul=True, residual=True)
     ids = m.ids()

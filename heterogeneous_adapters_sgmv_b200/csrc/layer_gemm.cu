@@ -517,16 +517,17 @@ int launch_layer_gemm(const lora_table *t, const lora_segments *seg, const void 
     if ((rc = encode_sw128(&p.tm_x, x, (uint64_t)t->h, (uint64_t)seg->T, (uint64_t)ldx, 128)) != LORA_OK ||
         (rc = encode_sw128(&p.tm_w, W, (uint64_t)t->h, (uint64_t)t->o, (uint64_t)ldw, (uint32_t)bn / 2)) != LORA_OK ||
         (rc = encode_sw128(&p.tm_y, static_cast<uint16_t *>(y) + y_off, (uint64_t)t->o, (uint64_t)seg->T, (uint64_t)ldy, 32)) !=
-            LORA_OK ||
-        (rc = encode_sw128(&p.tm_vhi, v_hi, kGRankPad, (uint64_t)seg->T, kGRankPad, 128)) != LORA_OK ||
-        (rc = encode_sw128(&p.tm_vlo, v_lo, kGRankPad, (uint64_t)seg->T, kGRankPad, 128)) != LORA_OK)
+            LORA_OK)
+        return rc;
+    if (v && ((rc = encode_sw128(&p.tm_vhi, v_hi, kGRankPad, (uint64_t)seg->T, kGRankPad, 128)) != LORA_OK ||
+              (rc = encode_sw128(&p.tm_vlo, v_lo, kGRankPad, (uint64_t)seg->T, kGRankPad, 128)) != LORA_OK))
         return rc;
     if (epi->mul && (rc = encode_sw128(&p.tm_mul, epi->mul, (uint64_t)t->o, (uint64_t)seg->T, (uint64_t)epi->ldmul, 32)) != LORA_OK)
         return rc;
     if (epi->residual &&
         (rc = encode_sw128(&p.tm_res, epi->residual, (uint64_t)t->o, (uint64_t)seg->T, (uint64_t)epi->ldres, 32)) != LORA_OK)
         return rc;
-    p.tm_B = static_cast<const uint8_t *>(t->d_tmaps_pfB) + (bn == 256 ? 0 : (size_t)t->n * 128);
+    if (v) p.tm_B = static_cast<const uint8_t *>(t->d_tmaps_pfB) + (bn == 256 ? 0 : (size_t)t->n * 128);
     p.seg_ptr = seg->seg_ptr;
     p.seg_adapter = seg->seg_adapter;
     p.num_segs = seg->num_segs;

@@ -109,7 +109,8 @@ int launch_base_gemm(const lora_table *t, const lora_segments *seg, const void *
 int launch_merge_finish(void *y, int64_t ldy, int32_t y_off, const float *yacc, int64_t ldacc, int32_t T, int32_t o,
                         int dtype, cudaStream_t s);
 // Layer products with their epilogue (layer_gemm.cu, layer_stream.cu).  `epi` is never null here.
-// launch_layer_gemm: as launch_base_gemm, contiguous segments, v from launch_prefill_shrink.
+// launch_layer_gemm: as launch_base_gemm, contiguous segments, v from launch_prefill_shrink (null: seg has
+// no segments).
 int launch_layer_gemm(const lora_table *t, const lora_segments *seg, const void *x, int64_t ldx, const void *W,
                       int64_t ldw, const lora_epilogue *epi, void *y, int64_t ldy, int32_t y_off, const void *v,
                       bool after_shrink, cudaStream_t s);

@@ -229,6 +229,15 @@ def test_bgmv_layer_same_bits_each_run_and_without_programmatic_launch():
     assert kernels_launched(lambda: m.bgmv(None)) == {"layer_stream_kernel"}
 
 
+@pytest.mark.parametrize("T,h,o", [(192, 128, 264), (257, 264, 136), (600, 72, 1032)])
+def test_bgmv_layer_without_adapters_in_large_batches(T, h, o):
+    """Without ids large batches take the tiles of the segment form; a table of any ranks will do."""
+    m = Layer(T, h, o, (3, 128), seed=9, act="silu", mul=True, residual=True, pad=8, y_off=16)
+    none = torch.full((T,), -1, dtype=torch.int32)
+    assert kernels_launched(lambda: m.bgmv(None)) == {"layer_gemm_kernel"}
+    m.check(m.y, none)
+
+
 # ------------------------------------------------------------------------------- segments
 
 def _ids_of(T, ptr, adapters):

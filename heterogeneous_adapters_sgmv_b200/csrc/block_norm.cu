@@ -244,6 +244,7 @@ struct RingShape {
     int32_t at[kOps];             // offset of each operand in its stage or area, -1: absent
     int32_t per_row;              // bit: the operand changes from row to row
     uint64_t wait_ns;
+    int32_t inject;               // test-only: rows are armed but never loaded
 };
 
 template <typename E, int NT, int V, bool AFTER>
@@ -287,7 +288,7 @@ ring_norm_kernel(const __grid_constant__ NormParams p, const __grid_constant__ R
         const uint32_t bar = smem_u32(&full[s]);
         row_id[s] = bad ? -2 : id;
         mbar_arrive_expect_tx(bar, bad ? 0u : (uint32_t)sh.stage_bytes);
-        if (bad) return;
+        if (bad || sh.inject) return;
 #pragma unroll
         for (int op = 0; op < kOps; ++op)
             if ((sh.per_row >> op) & 1)
@@ -407,6 +408,7 @@ int launch_ring(const NormParams &p, int dev, int sms, cudaStream_t s)
     RingShape sh = {};
     sh.row_bytes = p.d * (int)sizeof(E);
     sh.wait_ns = wait_limit_ns();
+    sh.inject = (int32_t)(options().inject_stall & 32);
     const bool gate = AFTER && p.res.gate_kind != LORA_GATE_NONE;
     const bool present[kOps] = {true,
                                 AFTER && p.res.residual,

@@ -56,6 +56,7 @@ struct LayerGemmParams {
     EpiParams epi;
     uint32_t *status;
     uint64_t wait_ns;
+    int32_t inject;               // test-only: a tile's first k-block is armed but never loaded
 };
 
 struct __align__(8) LayerGemmCtl {
@@ -236,11 +237,13 @@ __global__ void __launch_bounds__(kGThreads, 1) layer_gemm_kernel(const __grid_c
             return __all_sync(0xffffffffu, mbar_wait_hot(empty0 + s * 8, phase, p.status, p.wait_ns)) != 0;
         };
         // a stage's two loads: this CTA's half of the A side and of the B side
-        auto load = [&](const void *ta, int ca, const void *tb, int cb, int row, int col) {
+        auto load = [&](const void *ta, int ca, const void *tb, int cb, int row, int col, bool stall = false) {
             if (one) {
                 if (crank == 0) mbar_arrive_expect_tx(full0 + s * 8, 2 * kStage);
-                tma_load_2d_pair(ring0 + s * kStage, ta, ca, row, lead0 + s * 8);
-                tma_load_2d_pair(ring0 + s * kStage + kA, tb, cb, col, lead0 + s * 8);
+                if (!stall) {
+                    tma_load_2d_pair(ring0 + s * kStage, ta, ca, row, lead0 + s * 8);
+                    tma_load_2d_pair(ring0 + s * kStage + kA, tb, cb, col, lead0 + s * 8);
+                }
             }
             if (used < STAGES) ++used;
             if (++s == STAGES) {
@@ -259,7 +262,7 @@ __global__ void __launch_bounds__(kGThreads, 1) layer_gemm_kernel(const __grid_c
                 ok = free_stage();
                 if (!ok) break;
                 if (kb + 1 == nkb && one) ctl.last[s] = !more;
-                load(&p.tm_x, kb * kGK, &p.tm_w, kb * kGK, row, col);
+                load(&p.tm_x, kb * kGK, &p.tm_w, kb * kGK, row, col, p.inject && kb == 0);
             }
             while (ok && more) {
                 if (!waited) {
@@ -540,6 +543,7 @@ int launch_layer_gemm(const lora_table *t, const lora_segments *seg, const void 
     p.epi = epi_params(epi);
     p.status = t->d_status;
     p.wait_ns = wait_limit_ns();
+    p.inject = (int32_t)(options().inject_stall & 16);
 
     const int64_t run = std::min<int64_t>(pairs, tiles_of(bn));
     if (epi->mul && epi->residual) return bn == 256 ? launch_tiles<256, 2>(p, run, dev, s) : launch_tiles<128, 2>(p, run, dev, s);

@@ -240,28 +240,30 @@ struct LayerStreamParams {
     EpiParams epi;
     uint32_t *status;
     uint64_t wait_ns;
+    int32_t inject;               // test-only: the first k-block is armed but never loaded
 };
 
 struct __align__(16) LayerStreamCtl {
     uint64_t full[kLMaxStages], empty[kLMaxStages];
     uint64_t done, recv;
     uint32_t tmem_base, pad[3];
-    // behind it: v of the tokens at hand (kLVBytes for each half of the epilogue warps), then per token of
-    // the share its B_i and its rank (0: no adapter, -1: bad id)
+    // behind it: v of the tokens at hand (v_bytes for each half of the epilogue warps), then per token of the
+    // share its B_i and its rank (0: no adapter, -1: bad id)
 };
 
 constexpr int kLBatch = 4;                    // tokens an epilogue thread works on at a time
 // Bytes of v that a half of the epilogue warps holds at a time: at least a batch of tokens.
 constexpr int v_bytes(int epi_warps) { return epi_warps == 8 ? 8192 : 2048; }
-static_assert(v_bytes(4) / (LORA_MAX_RANK * 4) >= kLBatch && v_bytes(8) / (LORA_MAX_RANK * 4) >= 8, "a batch of tokens fits");
+static_assert(v_bytes(4) / (LORA_MAX_RANK * 4) >= kLBatch, "a batch of tokens fits");
 
-// The adapter terms of one thread's output column n, NB tokens at a time:
+// The adapter terms of one thread's output column n, a batch of tokens at a time:
 //   d[j] = sum_k B_j[n, k] v_j[k].
 // Rows of a rank that is a multiple of 8 are 16-byte aligned and read NP pieces of 8 a step, the step's
 // loads together (under a saturated memory system a load takes 2 to 4 us) and the first step's before v is
 // there; other rows are read element by element, the batch's together.
-template <int NB, int NP>
+template <int NP>
 struct ExpandRows {
+    static constexpr int NB = kLBatch;
     const int32_t *rank;        // per token; <= 0: none
     const void *const *B;
     int64_t n;
@@ -351,8 +353,9 @@ template <int S, int E, int CTAS>
 __global__ void __launch_bounds__((2 + E) * 32, CTAS)
 layer_stream_kernel(const __grid_constant__ LayerStreamParams p)
 {
-    // what the registers hold of B_i at a time: tokens and 16-byte pieces of their rows
-    constexpr int NB = kLBatch, NP = E == 4 || CTAS == 1 ? 4 : 2;
+    // 16-byte pieces of B_i's rows in registers, for each token of a batch: four where there are registers for
+    // them (4096 columns, 256 tokens, ranks to 64: 81 against 95 us with two)
+    constexpr int NP = E == 4 || CTAS == 1 ? 4 : 2;
     constexpr int H = E / 4;   // epilogue warps per TMEM lane quarter, each with its part of the tokens
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -409,11 +412,11 @@ layer_stream_kernel(const __grid_constant__ LayerStreamParams p)
         if (one)
             for (int kb = 0; kb < pre; ++kb) {
                 mbar_arrive_expect_tx(full0 + kb * 8, (uint32_t)stage_bytes);
-                tma_load_2d(ring0 + kb * stage_bytes, &p.tm_w, (kb0 + kb) * kLK, row0, full0 + kb * 8);
+                if (!p.inject || kb > 0) tma_load_2d(ring0 + kb * stage_bytes, &p.tm_w, (kb0 + kb) * kLK, row0, full0 + kb * 8);
             }
         if (!p.early) pdl_wait();
         if (one)
-            for (int kb = 0; kb < pre; ++kb)
+            for (int kb = p.inject ? 1 : 0; kb < pre; ++kb)
                 tma_load_2d(ring0 + kb * stage_bytes + kLWBytes, &p.tm_x, (kb0 + kb) * kLK, t0, full0 + kb * 8);
         int kb = pre, s = pre == p.stages ? 0 : pre;
         uint32_t phase = 0;
@@ -506,7 +509,7 @@ layer_stream_kernel(const __grid_constant__ LayerStreamParams p)
         }
         // While W streams: bias and adapter term of every output, kept in tensor memory behind the
         // accumulator.
-        ExpandRows<NB, NP> ex;
+        ExpandRows<NP> ex;
         ex.rank = tok_rank;
         ex.B = tok_B;
         ex.n = n;
@@ -514,7 +517,7 @@ layer_stream_kernel(const __grid_constant__ LayerStreamParams p)
         ex.end = i1;
         ex.load(i0, 0);
         float *vs = reinterpret_cast<float *>(v_buf + half * v_bytes(E));
-        const int at_once = p.ids ? v_bytes(E) / 4 / p.ldv / NB * NB : p.N;
+        const int at_once = p.ids ? v_bytes(E) / 4 / p.ldv / kLBatch * kLBatch : p.N;
         if (p.early) pdl_wait();   // v
         for (int c = i0; c < i1; c += at_once) {
             const int ce = min(i1, c + at_once);
@@ -538,15 +541,11 @@ layer_stream_kernel(const __grid_constant__ LayerStreamParams p)
                 }
                 named_bar_sync(2 + half, 128);
             }
-            for (int i = c; i < ce; i += NB) {
-                float d[NB];
-#pragma unroll
-                for (int j = 0; j < NB; ++j) d[j] = bias;
+            for (int i = c; i < ce; i += kLBatch) {
+                float d[kLBatch] = {bias, bias, bias, bias};
                 ex.run(i, vs + (i - c) * p.ldv, p.ldv, d);
                 __syncwarp();
-#pragma unroll
-                for (int j = 0; j < NB; j += 4)
-                    if (i + j < i1) tmem_st4(tmem_row + (uint32_t)(p.N + i + j), d[j], d[j + 1], d[j + 2], d[j + 3]);
+                tmem_st4(tmem_row + (uint32_t)(p.N + i), d[0], d[1], d[2], d[3]);
             }
         }
         // mul and residual of two batches, read ahead of their use
@@ -636,8 +635,8 @@ struct StreamShape {
 // 8.3 us with 8, 9.3 with 4), with adapters no more than make four CTAs for five SMs (64 tokens: 17.5 us with 4,
 // 18.9 with 8; 14336 outputs: 32.0 with 2, 36.4 with 1), since every CTA more waits for v and for its peers.
 // CTAs per SM: two where half an SM's shared memory holds three stages and half of its tensor memory the
-// accumulator with the adapter terms behind it, else one, as where there is no second CTA to put beside it.  One CTA alone
-// leaves 16 KB so that a CTA of the shrink fits beside it.
+// accumulator with the adapter terms behind it, else one, as where there is no second CTA to put beside it.
+// One CTA alone leaves 16 KB so that a CTA of the shrink fits beside it.
 StreamShape stream_shape(int T, int h, int o, int n_sms, bool adapters)
 {
     StreamShape sh;
@@ -816,6 +815,7 @@ int launch_layer_stream(const lora_table *t, const int32_t *ids, int32_t T, cons
     p.epi = epi_params(epi);
     p.status = t->d_status;
     p.wait_ns = wait_limit_ns();
+    p.inject = (int32_t)(options().inject_stall & 8);
     if (sh.E == 4) return sh.ctas == 2 ? launch_stream_width<4, 2>(p, sh, s, dev) : launch_stream_width<4, 1>(p, sh, s, dev);
     return sh.ctas == 2 ? launch_stream_width<8, 2>(p, sh, s, dev) : launch_stream_width<8, 1>(p, sh, s, dev);
 }

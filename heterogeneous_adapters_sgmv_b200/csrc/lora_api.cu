@@ -523,7 +523,7 @@ int lora_sgmv_base(const lora_table *t, const lora_segments *seg, const void *x,
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     void *v = static_cast<uint8_t *>(ws) + w.v;
     const bool shrink = seg->max_segs > 0;
-    if (shrink && (rc = launch_prefill_shrink(t, seg, x, ldx, v, true, 0, s)) != LORA_OK) return rc;
+    if (shrink && (rc = launch_prefill_shrink(t, seg, x, ldx, v, true, s)) != LORA_OK) return rc;
     return launch_base_gemm(t, seg, x, ldx, W, ldw, y, ldy, y_off, accumulate, v, shrink, s);
 }
 
@@ -730,7 +730,7 @@ int lora_sgmv_layer(const lora_table *t, const lora_segments *seg, const void *x
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     void *v = static_cast<uint8_t *>(ws) + w.v;
     const bool shrink = seg->max_segs > 0;
-    if (shrink && (rc = launch_prefill_shrink(t, seg, x, ldx, v, true, 0, s)) != LORA_OK) return rc;
+    if (shrink && (rc = launch_prefill_shrink(t, seg, x, ldx, v, true, s)) != LORA_OK) return rc;
     const lora_epilogue none = {};
     return launch_layer_gemm(t, seg, x, ldx, W, ldw, epi ? epi : &none, y, ldy, y_off, v, shrink, s);
 }

@@ -94,10 +94,9 @@ int launch_build_segments(const int32_t *ids, int32_t T, int32_t n, int32_t *per
 // Tensor maps of every adapter for the tcgen05 prefill path (no-op when the table does not qualify).
 int prefill_build_maps(lora_table *t);
 // tcgen05 shrink alone (contiguous segments, prefill-capable table): v receives the bf16 hi and
-// lo parts ([T, 64] each) of x . A_i^T, multiplied by s_i when fold_scale.  ksplit: 1 or 2 CTAs per
-// 128-token tile, or 0 for option "prefill_ksplit".
+// lo parts ([T, 64] each) of x . A_i^T, multiplied by s_i when fold_scale.
 int launch_prefill_shrink(const lora_table *t, const lora_segments *seg, const void *x, int64_t ldx, void *v,
-                          bool fold_scale, int ksplit, cudaStream_t s);
+                          bool fold_scale, cudaStream_t s);
 // Fused layer output (base_gemm.cu): y = (y if accumulate) + x W^T + the adapter term, from the
 // scale-folded intermediate v that launch_prefill_shrink wrote.
 // after_shrink: launch_prefill_shrink was the launch just before on `s` (lets the kernel start

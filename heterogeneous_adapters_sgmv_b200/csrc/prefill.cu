@@ -67,9 +67,9 @@ namespace {
 constexpr int kTileM = 128;          // tokens per tile
 constexpr int kTileN = 128;          // columns of o per expand tile
 constexpr int kBK = 64;              // columns of h per shrink k-block (128 bytes of bf16)
-constexpr int kStagesMax = 8;        // shrink pipeline depth, at most
+constexpr int kStagesMax = 4;        // shrink pipeline depth
 // (eight stages with the split of 4 measured slower: 17.4 against 16.3 us)
-__host__ __device__ constexpr int shrink_stages(int ks) { return ks <= 2 ? 8 : 4; }
+__host__ __device__ constexpr int shrink_stages(int) { return 4; }
 constexpr int kThreadsPF = 128;      // 4 warps: one TMEM lane quarter each
 constexpr int kMaxRankPF = 64;
 
@@ -918,10 +918,6 @@ int set_prefill_attributes()
     if (!attr_done[dev]) {
         if (cudaFuncSetAttribute(prefill_shrink_kernel<8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  shrink_smem(8)) != cudaSuccess ||
-            cudaFuncSetAttribute(prefill_shrink_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 shrink_smem(2)) != cudaSuccess ||
-            cudaFuncSetAttribute(prefill_shrink_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 shrink_smem(1)) != cudaSuccess ||
             cudaFuncSetAttribute(prefill_shrink_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  shrink_smem(4)) != cudaSuccess ||
             cudaFuncSetAttribute(prefill_expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kExpandSmem) !=
@@ -935,7 +931,7 @@ int set_prefill_attributes()
 // The tcgen05 shrink: clusters of KS CTAs (split of h), one cluster per 128-token tile of a
 // segment; the intermediate (times s_i when fold_scale) goes to v as bf16 hi + lo [T, 64] each.
 int launch_shrink_kernel(PrefillParams &p, const lora_table *t, const lora_segments *seg, const void *x, int64_t ldx,
-                         int ksplit, cudaStream_t s)
+                         cudaStream_t s)
 {
     const Options &opt = options();
     const int mt_bound = tile_bound(seg, p.min_len);
@@ -945,7 +941,7 @@ int launch_shrink_kernel(PrefillParams &p, const lora_table *t, const lora_segme
     if (p.perm && (rc = encode_sw128(&p.tmap_g, x, (uint64_t)t->h, (uint64_t)seg->T, (uint64_t)ldx, 1)) != LORA_OK)
         return rc;
     cudaLaunchConfig_t cfg = {};
-    const int KS = ksplit == 1 || ksplit == 2 ? ksplit : opt.prefill_ksplit == 8 ? 8 : 4;
+    const int KS = opt.prefill_ksplit == 8 ? 8 : 4;
     cfg.gridDim = dim3(KS * mt_bound);
     cfg.blockDim = dim3(kThreadsPF);
     cfg.dynamicSmemBytes = shrink_smem(KS);
@@ -963,10 +959,8 @@ int launch_shrink_kernel(PrefillParams &p, const lora_table *t, const lora_segme
     }
     cfg.attrs = attr;
     cfg.numAttrs = na;
-    const cudaError_t e = KS == 4   ? cudaLaunchKernelEx(&cfg, prefill_shrink_kernel<4>, p)
-                          : KS == 8 ? cudaLaunchKernelEx(&cfg, prefill_shrink_kernel<8>, p)
-                          : KS == 2 ? cudaLaunchKernelEx(&cfg, prefill_shrink_kernel<2>, p)
-                                    : cudaLaunchKernelEx(&cfg, prefill_shrink_kernel<1>, p);
+    const cudaError_t e = KS == 4 ? cudaLaunchKernelEx(&cfg, prefill_shrink_kernel<4>, p)
+                                  : cudaLaunchKernelEx(&cfg, prefill_shrink_kernel<8>, p);
     if (e != cudaSuccess) return LORA_ERR_CUDA;
     note_launch(kKernPrefillShrink);
     return LORA_OK;
@@ -975,14 +969,14 @@ int launch_shrink_kernel(PrefillParams &p, const lora_table *t, const lora_segme
 }  // namespace
 
 int launch_prefill_shrink(const lora_table *t, const lora_segments *seg, const void *x, int64_t ldx, void *v,
-                          bool fold_scale, int ksplit, cudaStream_t s)
+                          bool fold_scale, cudaStream_t s)
 {
     if (!prefill_supported(t)) return LORA_ERR_UNSUPPORTED;
     int rc = set_prefill_attributes();
     if (rc != LORA_OK) return rc;
     PrefillParams p = prefill_params(t, seg, v);
     p.fold_scale = fold_scale ? 1 : 0;
-    return launch_shrink_kernel(p, t, seg, x, ldx, ksplit, s);
+    return launch_shrink_kernel(p, t, seg, x, ldx, s);
 }
 
 int launch_prefill(const lora_table *t, const lora_segments *seg, const void *x, int64_t ldx, void *y, int64_t ldy,
@@ -1001,7 +995,7 @@ int launch_prefill(const lora_table *t, const lora_segments *seg, const void *x,
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return LORA_ERR_CUDA;
     const Options &opt = options();
-    if ((rc = launch_shrink_kernel(p, t, seg, x, ldx, 0, s)) != LORA_OK) return rc;
+    if ((rc = launch_shrink_kernel(p, t, seg, x, ldx, s)) != LORA_OK) return rc;
     // expand: persistent, one CTA per SM over all (128-token tile, 128-column tile) pairs
     if ((rc = encode_sw128(&p.tmap_vhi, p.v_hi, kMaxRankPF, (uint64_t)seg->T, kMaxRankPF, kTileM)) != LORA_OK ||
         (rc = encode_sw128(&p.tmap_vlo, p.v_lo, kMaxRankPF, (uint64_t)seg->T, kMaxRankPF, kTileM)) != LORA_OK)

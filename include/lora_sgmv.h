@@ -129,7 +129,7 @@ int lora_table_destroy(lora_table *table);
 int lora_table_info(const lora_table *table, int32_t *n_adapters, int32_t *h_in,
                     int32_t *h_out, int32_t *max_rank, int32_t *dtype);
 
-/* Bytes of device workspace that lora_sgmv and lora_bgmv need for T tokens (a multiple of
+/* Bytes of device workspace that lora_sgmv, lora_bgmv and the layer calls need for T tokens (a multiple of
  * 256; 0 is never returned). */
 size_t lora_workspace_bytes(const lora_table *table, int32_t T);
 
@@ -243,7 +243,9 @@ int lora_bgmv_merged(const lora_table *table, const int32_t *d_ids, const float 
  * of y with x, mul or residual is LORA_ERR_INVALID_ARG.  bias and W are weights: like a table's
  * A_i and B_i they may be read ahead of the stream's earlier work, so a call of this library that
  * is still in flight must not be writing them.
- * The layer and norm calls want the table's device to be the current one (LORA_ERR_INVALID_ARG). */
+ * The layer and norm calls want the table's device to be the current one (LORA_ERR_INVALID_ARG).  A
+ * workspace serves one call at a time: calls that may overlap on the GPU (other streams, captured
+ * graphs replayed side by side) need one each. */
 #define LORA_ACT_NONE 0
 #define LORA_ACT_RELU 1      /* max(z, 0)                                                        */
 #define LORA_ACT_GELU 2      /* z Phi(z), Phi the normal distribution function                   */
@@ -277,8 +279,9 @@ int lora_sgmv_layer(const lora_table *table, const lora_segments *seg, const voi
  * d_ids is [T] on the device, -1 for no adapter; NULL: no token has one (then ws may be NULL).  An
  * id outside [-1, n) latches LORA_STATUS_BAD_ID and leaves the token's row of y as it was.  A bf16
  * table of any rank up to LORA_MAX_RANK, without Sigma (else LORA_ERR_UNSUPPORTED); ws_bytes >=
- * lora_workspace_bytes(table, T).  Two launches (one without ids): the fp32 intermediate into the
- * workspace, then one pass over W. */
+ * lora_workspace_bytes(table, T).  Two launches: the fp32 intermediate into the workspace, then one
+ * pass over W.  Without ids one launch: that pass, or in large batches the product kernel of
+ * lora_sgmv_layer. */
 int lora_bgmv_layer(const lora_table *table, const int32_t *d_ids, int32_t T, const void *x,
                     int64_t ldx, const void *W, int64_t ldw, const lora_epilogue *epilogue, void *y,
                     int64_t ldy, int32_t y_offset, void *ws, size_t ws_bytes, void *stream);
@@ -378,7 +381,8 @@ const char *lora_status_string(int code);
  * path; 0 disables that path), "split" (1: lora_sgmv runs lora_shrink then lora_expand
  * through the workspace instead of the fused kernel), "wait_limit_ns" (bound of every
  * device-side wait of the following launches; 0: the default of about 2 s), "inject_stall"
- * (tests only: a bit mask, 1 decode kernels, 2 tcgen05 shrink, 4 tcgen05 expand, that arms one
+ * (tests only: a bit mask, 1 decode kernels, 2 tcgen05 shrink, 4 tcgen05 expand, 8 the weight pass
+ * of lora_bgmv_layer, 16 the product of lora_sgmv_layer, 32 the norms' row ring, that arms one
  * pipeline stage per unit or tile without ever loading it, so the bounded wait on it runs
  * out, LORA_STATUS_TIMEOUT is latched and the kernel drains its copies, releases tensor
  * memory and returns; results are then invalid), "tc_min_seg_len" (segments at least this

@@ -365,3 +365,20 @@ def test_layer_refuses_a_short_workspace_and_another_device():
         L.lora_bgmv_layer(m.table.handle, m.ids().cuda(), 9, m.x, 64, m.W, 64, None, m.y, 64, 0, m.ws, 64)
     assert e.value.code == L.LORA_ERR_WORKSPACE
     assert (m.y == 7.0).all()
+
+
+@pytest.mark.parametrize("bit,T,form", [(8, 5, "bgmv"), (8, 70, "bgmv"), (8, 300, "bgmv"), (16, 300, "sgmv")])
+def test_layer_wait_runs_out_then_recovers(bit, T, form):
+    """A stage that is armed and never loaded: with the bound at 20 ms the waits on it run out, the status
+    word says so, and the next call on the same table runs as if nothing had been."""
+    m = Layer(T, 1024, 392, (16, 8), seed=25, act="silu", mul=True, residual=True)
+    ptr, ads = [0, T // 2, T], [0, 1]
+    ids = _ids_of(T, ptr, ads)
+    call = (lambda: m.bgmv(ids)) if form == "bgmv" else (lambda: m.sgmv(m.segments(ptr, ads)))
+    with option("wait_limit_ns", 20_000_000), option("inject_stall", bit):
+        call()
+        torch.cuda.synchronize()
+    rc, word = L.lora_get_status(m.table.handle)
+    assert rc == L.LORA_ERR_TIMEOUT and word == L.LORA_STATUS_TIMEOUT
+    call()
+    m.check(m.y, ids, "after a timeout")

@@ -222,6 +222,71 @@ def test_layer_norm_of_a_large_mean():
     close(h, ref, off, m.half, "large mean")
 
 
+# many rows: persistent blocks with a ring in shared memory, whose depth falls with the width (four rows of
+# the narrow ones; where not even two fit, as of the widest rows in 32 bits with their weights, a block takes
+# one row); the last blocks get fewer rows than the first
+@pytest.mark.parametrize("dtype,T,d", [("bf16", 4001, 64), ("bf16", 1777, 1032), ("bf16", 2500, 2048),
+                                       ("bf16", 3003, 4096), ("bf16", 1800, 8200), ("bf16", 1777, 16384),
+                                       ("f32", 1901, 520), ("f32", 1777, 4096), ("f32", 1776, 16384)])
+def test_norms_of_many_rows(dtype, T, d):
+    m = Norms(T, d, dtype, seed=7, pad=8)
+    x, res = m.rnd(T, 2.0, 0.3), m.rnd(T, 3.0)
+    ids = m.ids()
+    zero = torch.zeros(T, d).double()
+    w, w2 = m.norm("layer", 1 + m.n), m.norm("rms", 1)
+    h = m.out()
+    names = kernels_launched(lambda: L.lora_norm_before(m.table.handle, ids.cuda(), T, d, x, x.stride(0), w["arg"], h,
+                                                        h.stride(0)))
+    assert names == {"ring_norm_kernel" if d * x.element_size() < 65536 else "block_norm_kernel"}
+    ref, off = norm_ref(x.cpu().double(), zero, w, ids)
+    close(h, ref, off, m.half, "before")
+    gate = m.rnd(T, 0.5, 0.5)
+    arg = L.make_residual(residual=res, ldres=res.stride(0), gate=gate, ldgate=gate.stride(0), gate_kind=L.LORA_GATE_TOKEN,
+                          res_scale=0.5, branch_scale=2.0)
+    r, h2 = m.out(), m.out()
+    bad = ids.clone()
+    bad[::97] = m.n
+    L.lora_norm_after(m.table.handle, bad.cuda(), T, d, x, x.stride(0), w["arg"], arg, r, r.stride(0), w2["arg"], h2,
+                      h2.stride(0))
+    assert L.lora_get_status(m.table.handle) == (L.LORA_ERR_DEVICE_STATUS, L.LORA_STATUS_BAD_ID)
+    g = gate.cpu().double()
+    u, off = ref * g * 2.0, off * g.abs() * 2.0
+    part = 0.5 * res.cpu().double()
+    off = off + 6 * U * u.abs() + 3 * U * (part.abs() + (part + u).abs())
+    ref2, off2 = norm_ref(part + u, off, w2, ids)
+    for got, want, o in ((r, part + u, off), (h2, ref2, off2)):
+        assert (got[::97] == 7.0).all()
+        keep = torch.arange(T) % 97 != 0
+        close(got[keep.cuda()], want[keep], o[keep], m.half, "after")
+    assert (r._base[:, d:] == 7.0).all() and (h._base[:, d:] == 7.0).all()
+
+
+def test_norm_rows_in_place_ahead_of_the_ring():
+    """Rows are read ahead of the block that writes them in place."""
+    T, d = 5000, 1024
+    m = Norms(T, d, seed=8)
+    w, w2, ids = m.norm("rms", 6), m.norm("layer", 6), m.ids().cuda()
+    z, s = m.rnd(T), m.rnd(T)
+    r, h = m.out(), m.out()
+    L.lora_norm_after(m.table.handle, ids, T, d, z, d, w["arg"], L.make_residual(s, d), r, d, w2["arg"], h, d)
+    L.lora_norm_after(m.table.handle, ids, T, d, z, d, w["arg"], L.make_residual(s, d), s, d, w2["arg"], z, d)
+    assert torch.equal(s, r) and torch.equal(z, h)
+
+
+def test_norm_wait_runs_out_then_recovers():
+    m = Norms(3000, 512, seed=9)
+    w, x = m.norm("rms"), m.rnd(3000)
+    good, h = m.out(), m.out()
+    L.lora_norm_before(m.table.handle, None, 3000, 512, x, 512, w["arg"], good, 512)
+    with option("wait_limit_ns", 20_000_000), option("inject_stall", 32):
+        L.lora_norm_before(m.table.handle, None, 3000, 512, x, 512, w["arg"], h, 512)
+        torch.cuda.synchronize()
+    assert L.lora_get_status(m.table.handle) == (L.LORA_ERR_TIMEOUT, L.LORA_STATUS_TIMEOUT)
+    assert (h == 7.0).all()
+    L.lora_norm_before(m.table.handle, None, 3000, 512, x, 512, w["arg"], h, 512)
+    assert torch.equal(h, good)
+
+
 # ------------------------------------------------------------------------------- together
 
 def test_a_block_of_norms_and_layers():

@@ -172,11 +172,12 @@ def _load():
 
 
 def _ptr(obj) -> Optional[int]:
-    if obj is None or type(obj) is int:
-        return obj
-    if isinstance(obj, int):
+    if obj is None:
+        return None
+    try:
+        return obj.data_ptr()
+    except AttributeError:
         return int(obj)
-    return obj.data_ptr()
 
 
 _torch_c = None
@@ -197,7 +198,9 @@ def _current_stream() -> int:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        return _current_stream()
+        if _torch_c is None:
+            return _current_stream()
+        return _torch_c._cuda_getCurrentRawStream(_torch_c._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
@@ -332,36 +335,39 @@ def make_residual(residual=None, ldres: int = 0, gate=None, ldgate: int = 0, gat
     return lora_residual(_ptr(residual), _ptr(gate), ldres, ldgate, res_scale, branch_scale, gate_kind, 0)
 
 
-def _ref(struct):
-    return None if struct is None else ctypes.byref(struct)
-
-
 def lora_sgmv_layer(table: int, seg: lora_segments, x, ldx: int, W, ldw: int, epilogue: Optional[lora_epilogue], y,
                     ldy: int, y_offset: int, ws=None, ws_bytes: int = 0, stream=None) -> None:
     """A whole layer over contiguous segments: x W^T + s_i B_i A_i x, then the epilogue (None: none)."""
-    _check(_load().lora_sgmv_layer(table, ctypes.byref(seg), _ptr(x), ldx, _ptr(W), ldw, _ref(epilogue), _ptr(y), ldy,
-                                   y_offset, _ptr(ws), ws_bytes, _stream(stream)), "lora_sgmv_layer")
+    rc = (_lib or _load()).lora_sgmv_layer(table, seg, _ptr(x), ldx, _ptr(W), ldw, epilogue, _ptr(y), ldy, y_offset,
+                                           _ptr(ws), ws_bytes, _stream(stream))
+    if rc:
+        raise LoraError(rc, "lora_sgmv_layer")
 
 
 def lora_bgmv_layer(table: int, ids, T: int, x, ldx: int, W, ldw: int, epilogue: Optional[lora_epilogue], y, ldy: int,
                     y_offset: int, ws=None, ws_bytes: int = 0, stream=None) -> None:
     """A whole layer driven by per-token ids (None: no token has an adapter)."""
-    _check(_load().lora_bgmv_layer(table, _ptr(ids), T, _ptr(x), ldx, _ptr(W), ldw, _ref(epilogue), _ptr(y), ldy,
-                                   y_offset, _ptr(ws), ws_bytes, _stream(stream)), "lora_bgmv_layer")
+    rc = (_lib or _load()).lora_bgmv_layer(table, _ptr(ids), T, _ptr(x), ldx, _ptr(W), ldw, epilogue, _ptr(y), ldy,
+                                           y_offset, _ptr(ws), ws_bytes, _stream(stream))
+    if rc:
+        raise LoraError(rc, "lora_bgmv_layer")
 
 
 def lora_norm_before(table: int, ids, T: int, d: int, x, ldx: int, norm: lora_norm, h, ldh: int, stream=None) -> None:
     """The norm before a block, each token with its adapter's gains: h = N(x)."""
-    _check(_load().lora_norm_before(table, _ptr(ids), T, d, _ptr(x), ldx, _ref(norm), _ptr(h), ldh, _stream(stream)),
-           "lora_norm_before")
+    rc = (_lib or _load()).lora_norm_before(table, _ptr(ids), T, d, _ptr(x), ldx, norm, _ptr(h), ldh, _stream(stream))
+    if rc:
+        raise LoraError(rc, "lora_norm_before")
 
 
 def lora_norm_after(table: int, ids, T: int, d: int, z, ldz: int, norm: Optional[lora_norm], residual: lora_residual,
                     r, ldr: int, next_norm: Optional[lora_norm] = None, h=None, ldh: int = 0, stream=None) -> None:
     """The norm after a block, gate and residual, and the next block's norm, in one pass:
     r = res_scale * residual + branch_scale * gate * N(z); h = N_next(r)."""
-    _check(_load().lora_norm_after(table, _ptr(ids), T, d, _ptr(z), ldz, _ref(norm), _ref(residual), _ptr(r), ldr,
-                                   _ref(next_norm), _ptr(h), ldh, _stream(stream)), "lora_norm_after")
+    rc = (_lib or _load()).lora_norm_after(table, _ptr(ids), T, d, _ptr(z), ldz, norm, residual, _ptr(r), ldr, next_norm,
+                                           _ptr(h), ldh, _stream(stream))
+    if rc:
+        raise LoraError(rc, "lora_norm_after")
 
 
 def lora_get_status(table: int, reset: bool = True, stream=None):

@@ -236,7 +236,8 @@ __global__ void __launch_bounds__(NT) block_norm_kernel(const __grid_constant__ 
 enum NormOperand { kOpX, kOpRes, kOpGate, kOpGain1, kOpShift1, kOpGain2, kOpShift2, kOps };
 constexpr int kNormStages = 4;
 // Blocks per SM: half its threads, or a quarter for the registers of the larger kernel.
-constexpr int ring_blocks(int nt, bool after) { return nt >= (after ? 512 : 1024) ? 1 : (after ? 768 : 1024) / nt; }
+template <int NT, bool AFTER>
+constexpr int kRingBlocks = NT >= (AFTER ? 512 : 1024) ? 1 : (AFTER ? 768 : 1024) / NT;
 
 struct RingShape {
     int32_t row_bytes, stages, stage_bytes;
@@ -248,7 +249,7 @@ struct RingShape {
 };
 
 template <typename E, int NT, int V, bool AFTER>
-__global__ void __launch_bounds__(NT, ring_blocks(NT, AFTER))
+__global__ void __launch_bounds__(NT, kRingBlocks<NT, AFTER>)
 ring_norm_kernel(const __grid_constant__ NormParams p, const __grid_constant__ RingShape sh)
 {
     extern __shared__ __align__(128) uint8_t smem[];
@@ -432,7 +433,7 @@ int launch_ring(const NormParams &p, int dev, int sms, cudaStream_t s)
         if (rows[op]) sh.per_row |= 1 << op;
     }
     // As many blocks as registers allow, as long as each has a ring of at least two stages.
-    int blocks = ring_blocks(NT, AFTER);
+    int blocks = kRingBlocks<NT, AFTER>;
     auto depth = [&](int n) { return (kShared / n - 2048 - sh.fixed_bytes) / sh.stage_bytes; };
     while (blocks > 1 && depth(blocks) < 2) --blocks;
     sh.stages = std::min(kNormStages, depth(blocks));

@@ -350,8 +350,7 @@ struct ExpandRows {
 // S CTAs of a cluster split the k axis; E epilogue warps (4 for small batches, which have few outputs, else
 // 8); CTAS to an SM.
 template <int S, int E, int CTAS>
-__global__ void __launch_bounds__((2 + E) * 32, CTAS)
-layer_stream_kernel(const __grid_constant__ LayerStreamParams p)
+__global__ void __launch_bounds__(E * 32 + 64, CTAS) layer_stream_kernel(const __grid_constant__ LayerStreamParams p)
 {
     // 16-byte pieces of B_i's rows in registers, for each token of a batch: four where there are registers for
     // them (4096 columns, 256 tokens, ranks to 64: 81 against 95 us with two)

@@ -10,9 +10,9 @@
 // row stays in registers as fp32, spread over the threads of one block (so a sum over the row is a
 // shuffle and one exchange through shared memory; the weights are read before the sums, which they do not
 // depend on).  Where there are many rows the blocks are
-// persistent (ring_norm_kernel): one thread brings the operands of the rows to come, the weights of each
-// row's adapter among them, into a ring in shared memory by bulk copies, and weights that serve all rows
-// once, so that no global load's latency lies between a row's sums.  The variance of a layer norm is taken from the centred values in
+// persistent (ring_norm_kernel): a warp of its own brings the operands of the rows to come, the weights of
+// each row's adapter among them, into a ring in shared memory by bulk copies, and weights that serve all
+// rows once, so that neither a global load's latency nor the issue of the copies lies between a row's sums.  The variance of a layer norm is taken from the centred values in
 // a second sum over the registers, not from the difference of two large sums.  h is computed from the
 // unrounded r, so that a fused call adds no rounding of its own.
 #include <algorithm>
@@ -20,6 +20,7 @@
 
 #include "lora_common.cuh"
 #include "lora_internal.h"
+#include "tcgen05.cuh"
 
 namespace lora {
 namespace {
@@ -57,7 +58,7 @@ template <> struct Vec<float> {
     }
 };
 
-// Sum over the block's NT threads, the same value in every thread.  `slot` must differ between
+// Sum over the block's first NT threads, the same value in every thread.  `slot` must differ between
 // consecutive calls (two are used in turn), so that one barrier per sum is enough.
 template <int NT>
 __device__ __forceinline__ float block_sum(float v, float (*part)[32], int slot)
@@ -67,7 +68,7 @@ __device__ __forceinline__ float block_sum(float v, float (*part)[32], int slot)
     if constexpr (NT > 32) {
         constexpr int kWarps = NT / 32;
         if ((threadIdx.x & 31) == 0) part[slot][threadIdx.x >> 5] = v;
-        __syncthreads();
+        named_bar_sync(1, NT);
         v = part[slot][threadIdx.x & (kWarps - 1)];
 #pragma unroll
         for (int d = kWarps / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
@@ -235,9 +236,10 @@ __global__ void __launch_bounds__(NT) block_norm_kernel(const __grid_constant__ 
 // what serves all rows).
 enum NormOperand { kOpX, kOpRes, kOpGate, kOpGain1, kOpShift1, kOpGain2, kOpShift2, kOps };
 constexpr int kNormStages = 4;
-// Blocks per SM: half its threads, or a quarter for the registers of the larger kernel.
-template <int NT, bool AFTER>
-constexpr int kRingBlocks = NT >= (AFTER ? 512 : 1024) ? 1 : (AFTER ? 768 : 1024) / NT;
+// Blocks per SM: what 64 registers a thread allow, or 80 for the larger kernel; 56 where 64 would leave one
+// large block alone (8192 wide: 16.2 against 17.9 us).
+template <int NT, int V, bool AFTER>
+constexpr int kRingBlocks = 65536 / (AFTER ? 80 : NT >= 512 && V <= 2 ? 56 : 64) / (NT + 32);
 
 struct RingShape {
     int32_t row_bytes, stages, stage_bytes;
@@ -248,80 +250,100 @@ struct RingShape {
     int32_t inject;               // test-only: rows are armed but never loaded
 };
 
+// Row `t` of operand `op` for a token with adapter row `w`.
+template <typename E>
+__device__ __forceinline__ const void *norm_source(const NormParams &p, int op, int64_t t, int64_t w)
+{
+    const void *b;
+    int64_t row;
+    switch (op) {
+    case kOpX: b = p.x, row = t * p.ldx; break;
+    case kOpRes: b = p.res.residual, row = t * p.res.ldres; break;
+    case kOpGate: b = p.res.gate, row = (p.res.gate_kind == LORA_GATE_TOKEN ? t : w) * p.res.ldgate; break;
+    case kOpGain1: b = p.norm.gain, row = w * p.norm.ld; break;
+    case kOpShift1: b = p.norm.shift, row = w * p.norm.ld; break;
+    case kOpGain2: b = p.next.gain, row = w * p.next.ld; break;
+    default: b = p.next.shift, row = w * p.next.ld; break;
+    }
+    return static_cast<const E *>(b) + row;
+}
+
+// NT threads work on rows; the warp behind them fetches.
 template <typename E, int NT, int V, bool AFTER>
-__global__ void __launch_bounds__(NT, kRingBlocks<NT, AFTER>)
+__global__ void __launch_bounds__(NT + 32, kRingBlocks<NT, V, AFTER>)
 ring_norm_kernel(const __grid_constant__ NormParams p, const __grid_constant__ RingShape sh)
 {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float part[2][32];
-    __shared__ uint64_t full[kNormStages], fixed;
+    __shared__ uint64_t full[kNormStages], empty[kNormStages], fixed;
     __shared__ int32_t row_id[kNormStages];
     uint8_t *ring = smem + sh.fixed_bytes;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < sh.stages; ++i) mbar_init(smem_u32(&full[i]), 1);
+        for (int i = 0; i < sh.stages; ++i) {
+            mbar_init(smem_u32(&full[i]), 1);
+            mbar_init(smem_u32(&empty[i]), 1);
+        }
         mbar_init(smem_u32(&fixed), 1);
         fence_mbar_init_cluster();
     }
+    __syncthreads();
     pdl_wait();
     pdl_launch_dependents();
     const int nvec = p.d / Vec<E>::kN;
-    // Row `t` of operand `op` for a token with adapter row `w`.
-    auto source = [&](int op, int64_t t, int64_t w) -> const void * {
-        const E *b;
-        int64_t row;
-        switch (op) {
-        case kOpX: b = static_cast<const E *>(p.x), row = t * p.ldx; break;
-        case kOpRes: b = static_cast<const E *>(p.res.residual), row = t * p.res.ldres; break;
-        case kOpGate:
-            b = static_cast<const E *>(p.res.gate);
-            row = (p.res.gate_kind == LORA_GATE_TOKEN ? t : w) * p.res.ldgate;
-            break;
-        case kOpGain1: b = static_cast<const E *>(p.norm.gain), row = w * p.norm.ld; break;
-        case kOpShift1: b = static_cast<const E *>(p.norm.shift), row = w * p.norm.ld; break;
-        case kOpGain2: b = static_cast<const E *>(p.next.gain), row = w * p.next.ld; break;
-        default: b = static_cast<const E *>(p.next.shift), row = w * p.next.ld; break;
-        }
-        return b + row;
-    };
-    // Thread 0: the operands of row t, whose adapter is `id`, into stage s.
-    auto fetch = [&](int64_t t, int s, int id) {
-        const bool bad = id < -1 || id >= p.n;   // nothing is read for it: the row stays as it was
-        const uint32_t bar = smem_u32(&full[s]);
-        row_id[s] = bad ? -2 : id;
-        mbar_arrive_expect_tx(bar, bad ? 0u : (uint32_t)sh.stage_bytes);
-        if (bad || sh.inject) return;
-#pragma unroll
-        for (int op = 0; op < kOps; ++op)
-            if ((sh.per_row >> op) & 1)
-                bulk_g2s(smem_u32(ring) + (uint32_t)(s * sh.stage_bytes + sh.at[op]), source(op, t, (int64_t)id + 1),
-                         (uint32_t)sh.row_bytes, bar);
-    };
-    int ahead = -1;   // thread 0: adapter of the next row to fetch
-    if (threadIdx.x == 0) {
-        mbar_arrive_expect_tx(smem_u32(&fixed), (uint32_t)sh.fixed_bytes);
-#pragma unroll
-        for (int op = 0; op < kOps; ++op)
-            if (sh.at[op] >= 0 && !((sh.per_row >> op) & 1))
-                bulk_g2s(smem_u32(smem) + (uint32_t)sh.at[op], source(op, 0, 0), (uint32_t)sh.row_bytes, smem_u32(&fixed));
-        int ids[kNormStages + 1];
-#pragma unroll
-        for (int i = 0; i <= kNormStages; ++i) {
-            const int64_t t = blockIdx.x + (int64_t)i * gridDim.x;
-            ids[i] = p.ids && i <= sh.stages && t < p.T ? p.ids[t] : -1;
-        }
-#pragma unroll
-        for (int i = 0; i < kNormStages; ++i) {
-            const int64_t t = blockIdx.x + (int64_t)i * gridDim.x;
-            if (i < sh.stages && t < p.T) fetch(t, i, ids[i]);
-            if (i < sh.stages) ahead = ids[i + 1];
-        }
-    }
-    __syncthreads();
-    bool ok = mbar_wait(smem_u32(&fixed), 0, p.status, sh.wait_ns);
     int s = 0;
     uint32_t phase = 0;
+    if (threadIdx.x >= NT) {
+        // ------------------------------------------------------------ fetch
+        const int lane = threadIdx.x & 31;
+        const bool one = elect_one();
+        if (one) {
+            mbar_arrive_expect_tx(smem_u32(&fixed), (uint32_t)sh.fixed_bytes);
+#pragma unroll
+            for (int op = 0; op < kOps; ++op)
+                if (sh.at[op] >= 0 && !((sh.per_row >> op) & 1))
+                    bulk_g2s(smem_u32(smem) + (uint32_t)sh.at[op], norm_source<E>(p, op, 0, 0), (uint32_t)sh.row_bytes,
+                             smem_u32(&fixed));
+        }
+        int ids = -1, i = 0;   // ids: lane l holds that of the l-th of the next 32 rows
+        for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, ++i) {
+            if (p.ids && (i & 31) == 0) {
+                const int64_t mine = t + (int64_t)lane * gridDim.x;
+                ids = mine < p.T ? p.ids[mine] : -1;
+            }
+            const int id = __shfl_sync(0xffffffffu, ids, i & 31);
+            if (!__all_sync(0xffffffffu, mbar_wait_hot(smem_u32(&empty[s]), phase ^ 1, p.status, sh.wait_ns))) break;
+            if (one) {
+                const bool bad = id < -1 || id >= p.n;   // nothing is read for it: the row stays as it was
+                const uint32_t bar = smem_u32(&full[s]);
+                row_id[s] = bad ? -2 : id;
+                mbar_arrive_expect_tx(bar, bad ? 0u : (uint32_t)sh.stage_bytes);
+                if (!bad && !sh.inject)
+#pragma unroll
+                    for (int op = 0; op < kOps; ++op)
+                        if ((sh.per_row >> op) & 1)
+                            bulk_g2s(smem_u32(ring) + (uint32_t)(s * sh.stage_bytes + sh.at[op]),
+                                     norm_source<E>(p, op, t, (int64_t)id + 1), (uint32_t)sh.row_bytes, bar);
+            }
+            __syncwarp();
+            if (++s == sh.stages) {
+                s = 0;
+                phase ^= 1;
+            }
+        }
+        // the copies under way have landed before the block ends
+        for (int k = 0; k < min(i, sh.stages); ++k) {
+            if (--s < 0) {
+                s = sh.stages - 1;
+                phase ^= 1;
+            }
+            mbar_wait(smem_u32(&full[s]), phase, p.status, sh.wait_ns);
+        }
+        mbar_wait(smem_u32(&fixed), 0, p.status, sh.wait_ns);
+        return;
+    }
+    // ------------------------------------------------------------ rows
+    bool ok = mbar_wait(smem_u32(&fixed), 0, p.status, sh.wait_ns);
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
-        const int64_t behind = t + (int64_t)sh.stages * gridDim.x;   // the row that takes this stage next
         ok = mbar_wait(smem_u32(&full[s]), phase, p.status, sh.wait_ns) && ok;
         auto operand = [&](int op) {
             return reinterpret_cast<const uint4 *>(((sh.per_row >> op) & 1 ? ring + s * sh.stage_bytes : smem) + sh.at[op]);
@@ -353,30 +375,16 @@ ring_norm_kernel(const __grid_constant__ NormParams p, const __grid_constant__ R
                 for (int j = 0; j < V; ++j) join<E>(p.res, f.f[j], gate.w[j], in.w[j]);
                 if (p.r) f.store(p.r, t * p.ldr, nvec);
                 if (p.h) {
-                    if (NT > 32 && p.norm.kind) __syncthreads();   // the first norm's sums are read by all
+                    if (NT > 32 && p.norm.kind) named_bar_sync(1, NT);   // the first norm's sums are read by all
                     weights(p.next, kOpGain2, w);
                     f.normalise(p.next, w, p.d, nvec, part);
                     f.store(p.h, t * p.ldh, nvec);
                 }
             }
         }
-        // The stage and the sums have been read by all.  A wait that ran out anywhere ends the block, once
-        // its copies have landed.
-        if (!__syncthreads_and(ok)) {
-            if (threadIdx.x == 0)
-                for (int i = 0; i < sh.stages; ++i) {
-                    if (t + (int64_t)i * gridDim.x < p.T) mbar_wait(smem_u32(&full[s]), phase, p.status, sh.wait_ns);
-                    if (++s == sh.stages) {
-                        s = 0;
-                        phase ^= 1;
-                    }
-                }
-            return;
-        }
-        if (threadIdx.x == 0 && behind < p.T) {
-            fetch(behind, s, ahead);
-            if (p.ids && behind + gridDim.x < p.T) ahead = p.ids[behind + gridDim.x];
-        }
+        // The stage and the sums have been read by all.  A wait that ran out in any thread ends them all.
+        if (!named_bar_and(2, NT, ok)) return;
+        if (threadIdx.x == 0) mbar_arrive(smem_u32(&empty[s]));
         if (++s == sh.stages) {
             s = 0;
             phase ^= 1;
@@ -433,7 +441,7 @@ int launch_ring(const NormParams &p, int dev, int sms, cudaStream_t s)
         if (rows[op]) sh.per_row |= 1 << op;
     }
     // As many blocks as registers allow, as long as each has a ring of at least two stages.
-    int blocks = kRingBlocks<NT, AFTER>;
+    int blocks = kRingBlocks<NT, V, AFTER>;
     auto depth = [&](int n) { return (kShared / n - 2048 - sh.fixed_bytes) / sh.stage_bytes; };
     while (blocks > 1 && depth(blocks) < 2) --blocks;
     sh.stages = std::min(kNormStages, depth(blocks));
@@ -445,7 +453,7 @@ int launch_ring(const NormParams &p, int dev, int sms, cudaStream_t s)
     });
     if (attr_rc[dev] != cudaSuccess) return LORA_ERR_CUDA;
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = norm_config(std::min<int64_t>(p.T, (int64_t)blocks * sms), NT,
+    const cudaLaunchConfig_t cfg = norm_config(std::min<int64_t>(p.T, (int64_t)blocks * sms), NT + 32,
                                                (size_t)(sh.fixed_bytes + sh.stages * sh.stage_bytes), s, attr);
     if (cudaLaunchKernelEx(&cfg, kern, p, sh) != cudaSuccess) return LORA_ERR_CUDA;
     note_launch(kKernRingNorm);
@@ -467,14 +475,16 @@ constexpr int kRingRowsPerSm = 12;
 
 // NT threads with V vectors each for a row: NT1, V1 where a block takes one row (latency counts, so many
 // threads), NT2, V2 for persistent blocks (rows side by side count, so few; but not more than two vectors a
-// thread, whose registers spill otherwise).
+// thread while rows are short enough, whose registers spill otherwise; 0: none).
 template <typename E, int NT1, int V1, int NT2, int V2>
 int launch_one(const NormParams &p, bool after, int dev, int sms, cudaStream_t s)
 {
-    if (p.T >= kRingRowsPerSm * sms) {
-        const int rc = after ? launch_ring<E, NT2, V2, true>(p, dev, sms, s) : launch_ring<E, NT2, V2, false>(p, dev, sms, s);
-        if (rc != LORA_ERR_UNSUPPORTED) return rc;
-    }
+    if constexpr (NT2 > 0)
+        if (p.T >= kRingRowsPerSm * sms) {
+            const int rc =
+                after ? launch_ring<E, NT2, V2, true>(p, dev, sms, s) : launch_ring<E, NT2, V2, false>(p, dev, sms, s);
+            if (rc != LORA_ERR_UNSUPPORTED) return rc;
+        }
     return after ? launch_kernel<E, NT1, V1, true>(p, s) : launch_kernel<E, NT1, V1, false>(p, s);
 }
 
@@ -493,8 +503,8 @@ int launch_typed(const NormParams &p, bool after, cudaStream_t s)
     if (nvec <= 256) return launch_one<E, 256, 1, 128, 2>(p, after, dev, sms[dev], s);
     if (nvec <= 512) return launch_one<E, 256, 2, 256, 2>(p, after, dev, sms[dev], s);
     if (nvec <= 1024) return launch_one<E, 512, 2, 512, 2>(p, after, dev, sms[dev], s);
-    if (nvec <= 2048) return launch_one<E, 512, 4, 1024, 2>(p, after, dev, sms[dev], s);
-    if constexpr (LORA_MAX_NORM_WIDTH > 2048 * Vec<E>::kN) return launch_one<E, 1024, 4, 1024, 4>(p, after, dev, sms[dev], s);
+    if (nvec <= 2048) return launch_one<E, 512, 4, 512, 4>(p, after, dev, sms[dev], s);
+    if constexpr (LORA_MAX_NORM_WIDTH > 2048 * Vec<E>::kN) return launch_one<E, 1024, 4, 0, 0>(p, after, dev, sms[dev], s);
     return LORA_ERR_UNSUPPORTED;
 }
 static_assert(LORA_MAX_NORM_WIDTH <= 1024 * 4 * Vec<float>::kN && LORA_MAX_NORM_WIDTH <= 2048 * Vec<__nv_bfloat16>::kN,

@@ -38,7 +38,7 @@ namespace {
 
 constexpr int kGM = 256;                      // tokens per tile, 128 in each CTA
 constexpr int kGK = 64;                       // k-block: 64 bf16 = one 128-byte swizzled row
-constexpr int kGMaxStages = 8;
+constexpr int kGMaxStages = 6;
 constexpr int kGPiece = 32 * 128;             // bytes of an epilogue piece: 32 rows of 64 columns
 constexpr int kGEpiWarps = 8;
 constexpr int kGThreads = (2 + kGEpiWarps) * 32;
@@ -177,6 +177,10 @@ __device__ __forceinline__ void combine(const uint8_t *tile, int row, int c0, fl
     }
 }
 
+// k-blocks of 64 in a stage: a narrow tile's products take half the time, so each wait and each commit has to
+// serve two of them (one: 200 ns a k-block where the tensor cores need 135).
+constexpr int k_blocks(int bn) { return bn == 256 ? 1 : 2; }
+
 // BN: output columns per tile, 256, or 128 where those fill the SMs better.
 template <int BN, int STAGES>
 __global__ void __launch_bounds__(kGThreads, 1) layer_gemm_kernel(const __grid_constant__ LayerGemmParams p)
@@ -189,7 +193,9 @@ __global__ void __launch_bounds__(kGThreads, 1) layer_gemm_kernel(const __grid_c
     const int MT = (p.T + kGM - 1) / kGM, NT = (p.o + BN - 1) / BN;
     const int nkb = (p.h + kGK - 1) / kGK;
     const int total = MT * NT;
-    constexpr int kA = 128 * 128, kB = BN / 2 * 128, kStage = kA + kB;   // bytes of the A and B side of a stage
+    constexpr int kA = 128 * 128, kB = BN / 2 * 128, kSub = kA + kB;   // bytes of the A and B side of a k-block
+    constexpr int KB = k_blocks(BN), kStage = KB * kSub;               // k-blocks and bytes of a stage
+    const int nst = (nkb + KB - 1) / KB;                               // stages of a tile's base product
     const int nops = (p.epi.mul != nullptr) + (p.epi.res != nullptr), tiles = nops > 1 ? 2 : 1;
     uint8_t *pieces = ring + (STAGES * kStage + 1023) / 1024 * 1024;   // `tiles` for each epilogue warp
     LayerGemmCtl &ctl = *reinterpret_cast<LayerGemmCtl *>(pieces + kGEpiWarps * tiles * kGPiece);
@@ -236,15 +242,18 @@ __global__ void __launch_bounds__(kGThreads, 1) layer_gemm_kernel(const __grid_c
         auto free_stage = [&]() {
             return __all_sync(0xffffffffu, mbar_wait_hot(empty0 + s * 8, phase, p.status, p.wait_ns)) != 0;
         };
-        // a stage's two loads: this CTA's half of the A side and of the B side
-        auto load = [&](const void *ta, int ca, const void *tb, int cb, int row, int col, bool stall = false) {
+        // arms the stage and moves on; a k-block's two loads: this CTA's half of the A side and of the B side
+        auto arm = [&]() {
+            if (crank == 0 && one) mbar_arrive_expect_tx(full0 + s * 8, 2 * kStage);
+        };
+        auto load = [&](int u, const void *ta, int ca, const void *tb, int cb, int row, int col) {
+            const uint32_t at = ring0 + s * kStage + u * kSub;
             if (one) {
-                if (crank == 0) mbar_arrive_expect_tx(full0 + s * 8, 2 * kStage);
-                if (!stall) {
-                    tma_load_2d_pair(ring0 + s * kStage, ta, ca, row, lead0 + s * 8);
-                    tma_load_2d_pair(ring0 + s * kStage + kA, tb, cb, col, lead0 + s * 8);
-                }
+                tma_load_2d_pair(at, ta, ca, row, lead0 + s * 8);
+                tma_load_2d_pair(at + kA, tb, cb, col, lead0 + s * 8);
             }
+        };
+        auto next_stage = [&]() {
             if (used < STAGES) ++used;
             if (++s == STAGES) {
                 s = 0;
@@ -258,11 +267,16 @@ __global__ void __launch_bounds__(kGThreads, 1) layer_gemm_kernel(const __grid_c
             int lo, hi, a;
             sc.begin(p, tile_row, tile_row + kGM);
             bool more = sc.next(p, &lo, &hi, &a);
-            for (int kb = 0; kb < nkb; ++kb) {
+            for (int st = 0; st < nst; ++st) {
                 ok = free_stage();
                 if (!ok) break;
-                if (kb + 1 == nkb && one) ctl.last[s] = !more;
-                load(&p.tm_x, kb * kGK, &p.tm_w, kb * kGK, row, col, p.inject && kb == 0);
+                if (st + 1 == nst && one) ctl.last[s] = !more;
+                arm();
+                if (!(p.inject && st == 0))
+#pragma unroll
+                    for (int u = 0; u < KB; ++u)   // columns past h are zero-filled
+                        load(u, &p.tm_x, (st * KB + u) * kGK, &p.tm_w, (st * KB + u) * kGK, row, col);
+                next_stage();
             }
             while (ok && more) {
                 if (!waited) {
@@ -272,15 +286,18 @@ __global__ void __launch_bounds__(kGThreads, 1) layer_gemm_kernel(const __grid_c
                 const int lo1 = lo, hi1 = hi;
                 const void *tb = p.tm_B + (size_t)a * 128;
                 more = sc.next(p, &lo, &hi, &a);
-                for (int part = 0; part < 2; ++part) {   // hi, lo
+                for (int part = 0; part < 2; part += KB) {   // hi, lo
                     ok = free_stage();
                     if (!ok) break;
                     if (one) {
                         ctl.lo[s] = (int16_t)lo1;
                         ctl.hi[s] = (int16_t)hi1;
-                        ctl.last[s] = part == 1 && !more;
+                        ctl.last[s] = part + KB == 2 && !more;
                     }
-                    load(part ? &p.tm_vlo : &p.tm_vhi, 0, tb, 0, row, col);
+                    arm();
+#pragma unroll
+                    for (int u = 0; u < KB; ++u) load(u, part + u ? &p.tm_vlo : &p.tm_vhi, 0, tb, 0, row, col);
+                    next_stage();
                 }
             }
         }
@@ -318,18 +335,21 @@ __global__ void __launch_bounds__(kGThreads, 1) layer_gemm_kernel(const __grid_c
                     break;
                 tc_fence_after();
                 const uint32_t acc = tmem + (uint32_t)(ab * BN);
-                // nkb k-blocks of the base product, then as many of adapters as the producer says
+                // nst stages of the base product, then as many of adapters as the producer says
                 bool last = false;
-                for (int kb = 0; !last; ++kb) {
+                for (int st = 0; !last; ++st) {
                     ok = __all_sync(0xffffffffu, mbar_wait_hot(full0 + s * 8, phase, p.status, p.wait_ns));
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t ad = ad0 + (uint64_t)(s * (kStage >> 4)), bd = bd0 + (uint64_t)(s * (kStage >> 4));
-                    if (kb < nkb) {
+                    if (st < nst) {
                         if (one) {
 #pragma unroll
-                            for (int k = 0; k < kGK / 16; ++k)
-                                umma_bf16_pair(acc, ad + 2 * k, bd + 2 * k, idesc, (kb | k) ? 1u : 0u);
+                            for (int u = 0; u < KB; ++u)
+#pragma unroll
+                                for (int k = 0; k < kGK / 16; ++k)
+                                    umma_bf16_pair(acc, ad + u * (kSub >> 4) + 2 * k, bd + u * (kSub >> 4) + 2 * k, idesc,
+                                                   (st | u | k) ? 1u : 0u);
                             umma_commit_pair(empty0 + s * 8);
                         }
                     } else {
@@ -337,11 +357,15 @@ __global__ void __launch_bounds__(kGThreads, 1) layer_gemm_kernel(const __grid_c
                         rows_off(ctl.lo[s], ctl.hi[s], off);
                         if (one) {
 #pragma unroll
-                            for (int k = 0; k < kGK / 16; ++k) umma_bf16_pair_rows(acc, ad + 2 * k, bd + 2 * k, idesc, off);
+                            for (int u = 0; u < KB; ++u)
+#pragma unroll
+                                for (int k = 0; k < kGK / 16; ++k)
+                                    umma_bf16_pair_rows(acc, ad + u * (kSub >> 4) + 2 * k, bd + u * (kSub >> 4) + 2 * k, idesc,
+                                                        off);
                             umma_commit_pair(empty0 + s * 8);
                         }
                     }
-                    if (kb + 1 >= nkb) last = __all_sync(0xffffffffu, ctl.last[s] != 0);
+                    if (st + 1 >= nst) last = __all_sync(0xffffffffu, ctl.last[s] != 0);
                     if (++s == STAGES) {
                         s = 0;
                         phase ^= 1;
@@ -452,12 +476,12 @@ __global__ void __launch_bounds__(kGThreads, 1) layer_gemm_kernel(const __grid_c
 // and residual), the control block.
 constexpr int gemm_smem(int bn, int stages, int tiles)
 {
-    return stages * (128 * 128 + bn / 2 * 128) + kGEpiWarps * tiles * kGPiece + (int)sizeof(LayerGemmCtl) + 2048;
+    return stages * k_blocks(bn) * (128 * 128 + bn / 2 * 128) + kGEpiWarps * tiles * kGPiece + (int)sizeof(LayerGemmCtl) + 2048;
 }
 // The deepest rings that fit beside one and beside two tiles.
-constexpr int gemm_stages(int bn, int tiles) { return bn == 256 ? (tiles == 2 ? 5 : 6) : (tiles == 2 ? 6 : 8); }
+constexpr int gemm_stages(int bn, int tiles) { return bn == 256 ? (tiles == 2 ? 5 : 6) : (tiles == 2 ? 3 : 4); }
 static_assert(gemm_smem(256, 6, 1) <= 227 * 1024 && gemm_smem(256, 5, 2) <= 227 * 1024, "shared memory");
-static_assert(gemm_smem(128, 8, 1) <= 227 * 1024 && gemm_smem(128, 6, 2) <= 227 * 1024, "shared memory");
+static_assert(gemm_smem(128, 4, 1) <= 227 * 1024 && gemm_smem(128, 3, 2) <= 227 * 1024, "shared memory");
 
 template <int BN, int TILES>
 int launch_tiles(const LayerGemmParams &p, int64_t pairs, int dev, cudaStream_t s)

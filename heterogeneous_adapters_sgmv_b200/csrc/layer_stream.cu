@@ -247,13 +247,13 @@ struct __align__(16) LayerStreamCtl {
     uint64_t full[kLMaxStages], empty[kLMaxStages];
     uint64_t done, recv;
     uint32_t tmem_base, pad[3];
-    // behind it: v of the tokens at hand (v_bytes for each half of the epilogue warps), then per token of the
+    // behind it: v of the tokens at hand (v_bytes for each four epilogue warps), then per token of the
     // share its B_i and its rank (0: no adapter, -1: bad id)
 };
 
 constexpr int kLBatch = 4;                    // tokens an epilogue thread works on at a time
-// Bytes of v that a half of the epilogue warps holds at a time: at least a batch of tokens.
-constexpr int v_bytes(int epi_warps) { return epi_warps == 8 ? 8192 : 2048; }
+// Bytes of v that four epilogue warps hold at a time: at least a batch of tokens.
+constexpr int v_bytes(int epi_warps) { return epi_warps == 4 ? 2048 : epi_warps == 8 ? 8192 : 4096; }
 static_assert(v_bytes(4) / (LORA_MAX_RANK * 4) >= kLBatch, "a batch of tokens fits");
 
 // The adapter terms of one thread's output column n, a batch of tokens at a time:
@@ -347,14 +347,13 @@ struct ExpandRows {
     }
 };
 
-// S CTAs of a cluster split the k axis; E epilogue warps (4 for small batches, which have few outputs, else
-// 8); CTAS to an SM.
+// S CTAs of a cluster split the k axis; E epilogue warps (see stream_shape); CTAS to an SM.
 template <int S, int E, int CTAS>
 __global__ void __launch_bounds__(E * 32 + 64, CTAS) layer_stream_kernel(const __grid_constant__ LayerStreamParams p)
 {
     // 16-byte pieces of B_i's rows in registers, for each token of a batch: four where there are registers for
     // them (4096 columns, 256 tokens, ranks to 64: 81 against 95 us with two)
-    constexpr int NP = E == 4 || CTAS == 1 ? 4 : 2;
+    constexpr int NP = E == 4 || (E == 8 && CTAS == 1) ? 4 : 2;
     constexpr int H = E / 4;   // epilogue warps per TMEM lane quarter, each with its part of the tokens
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -470,11 +469,11 @@ __global__ void __launch_bounds__(E * 32 + 64, CTAS) layer_stream_kernel(const _
     } else {
         // ------------------------------------------------------------ epilogue
         // lane = row of W; this thread's tokens are [i0, i1) of the share
-        const int q = warp & 3, half = (warp - 2) >> 2, et = tid - 64;
+        const int q = warp & 3, part = (warp - 2) >> 2, et = tid - 64;
         const int m = q * 32 + lane, n = row0 + m;
         const bool col_ok = n < p.o;
         const int hs = (p.share / H + kLBatch - 1) / kLBatch * kLBatch;
-        const int i0 = half * hs, i1 = min(tb - ta, i0 + hs);
+        const int i0 = part * hs, i1 = min(tb - ta, i0 + hs);
         const uint32_t tmem_row = tmem + ((uint32_t)(q * 32) << 16);
         const int64_t tok0 = t0 + ta;
         if (!p.early) pdl_wait();   // ids may come from the kernel before
@@ -515,13 +514,13 @@ __global__ void __launch_bounds__(E * 32 + 64, CTAS) layer_stream_kernel(const _
         ex.col_ok = col_ok;
         ex.end = i1;
         ex.load(i0, 0);
-        float *vs = reinterpret_cast<float *>(v_buf + half * v_bytes(E));
+        float *vs = reinterpret_cast<float *>(v_buf + part * v_bytes(E));
         const int at_once = p.ids ? v_bytes(E) / 4 / p.ldv / kLBatch * kLBatch : p.N;
         if (p.early) pdl_wait();   // v
         for (int c = i0; c < i1; c += at_once) {
             const int ce = min(i1, c + at_once);
             if (p.ids) {
-                if (c > i0) named_bar_sync(2 + half, 128);   // the last tokens' v is done with
+                if (c > i0) named_bar_sync(2 + part, 128);   // the last tokens' v is done with
                 const float4 *src = reinterpret_cast<const float4 *>(p.v + (tok0 + c) * p.ldv);
                 for (int e = et & 127; e < (ce - c) * p.ldv / 4; e += 128) {
                     float4 f[kVParts];
@@ -538,7 +537,7 @@ __global__ void __launch_bounds__(E * 32 + 64, CTAS) layer_stream_kernel(const _
                         }
                     reinterpret_cast<float4 *>(vs)[e] = f[0];
                 }
-                named_bar_sync(2 + half, 128);
+                named_bar_sync(2 + part, 128);
             }
             for (int i = c; i < ce; i += kLBatch) {
                 float d[kLBatch] = {bias, bias, bias, bias};
@@ -568,7 +567,7 @@ __global__ void __launch_bounds__(E * 32 + 64, CTAS) layer_stream_kernel(const _
             if (p.alias) cluster_arrive_release();
             cluster_wait_acquire();
             // partial sums of the tokens that other CTAs finish, four tokens of a row at a time
-            for (int c = half * 16; ok && c < nv; c += 16 * H) {
+            for (int c = part * 16; ok && c < nv; c += 16 * H) {
                 float f[16];
                 tmem_ld16(tmem_row + (uint32_t)c, f);
 #pragma unroll
@@ -629,50 +628,6 @@ struct StreamShape {
     int N, NT, S, E, ctas, stages, share, ncols, recv, alias, smem;
 };
 
-// Tokens per tile: all of them up to 256 (rounded up to the MMA's 16), else equal tiles of at most
-// 256.  Clusters: up to 8 CTAs split k, without adapters as many as fit two to an SM (4096 -> 4096, one token:
-// 8.3 us with 8, 9.3 with 4), with adapters no more than make four CTAs for five SMs (64 tokens: 17.5 us with 4,
-// 18.9 with 8; 14336 outputs: 32.0 with 2, 36.4 with 1), since every CTA more waits for v and for its peers.
-// CTAs per SM: two where half an SM's shared memory holds three stages and half of its tensor memory the
-// accumulator with the adapter terms behind it, else one, as where there is no second CTA to put beside it.
-// One CTA alone leaves 16 KB so that a CTA of the shrink fits beside it.
-StreamShape stream_shape(int T, int h, int o, int n_sms, bool adapters)
-{
-    StreamShape sh;
-    sh.NT = (T + kLMaxN - 1) / kLMaxN;
-    const int per = (T + sh.NT - 1) / sh.NT;
-    sh.N = (per + 15) & ~15;
-    const int stage = kLWBytes + sh.N * 128;
-    const int64_t tiles = (int64_t)((o + kLM - 1) / kLM) * sh.NT;
-    const int nkb = (h + kLK - 1) / kLK;
-    for (int ctas = 2;; --ctas) {
-        sh.E = sh.N <= 32 ? 4 : 8;
-        sh.ctas = ctas;
-        const int H = sh.E / 4;
-        sh.S = 1;
-        while (sh.S < 8 && tiles * sh.S * 2 <= (int64_t)n_sms * ctas && sh.S * 2 <= nkb &&
-               !(adapters && tiles * sh.S * 5 >= 4ll * n_sms))
-            sh.S *= 2;
-        // S shares cover a whole tile (N, which is more than `per` when there are several)
-        sh.share = ((std::min(sh.N, T) + sh.S - 1) / sh.S + kLBatch - 1) / kLBatch * kLBatch;
-        const int hs = (sh.share / H + kLBatch - 1) / kLBatch * kLBatch;
-        sh.ncols = 32;
-        while (sh.ncols < sh.N + H * hs) sh.ncols *= 2;
-        const int ctl = 1024 + (int)sizeof(LayerStreamCtl) + H * v_bytes(sh.E) + sh.share * 12;
-        const int recv = (sh.S - 1) * sh.share * kLM * 4;
-        const int room = (ctas == 1 ? 210 : 227 / ctas - 1) * 1024 - ctl;
-        // the peers' partial sums beside the ring where that leaves it three stages, else in it
-        sh.alias = (room - recv) / stage < 3;
-        sh.stages = std::min(kLMaxStages, (room - (sh.alias ? 0 : recv)) / stage);
-        if (sh.alias && sh.stages * stage < recv) sh.stages = 0;
-        if (ctas > 1 && (sh.stages < 3 || sh.ncols > 512 / ctas || tiles * sh.S <= n_sms)) continue;
-        sh.stages = std::max(sh.alias ? (recv + stage - 1) / stage : 1, std::min(sh.stages, (nkb + sh.S - 1) / sh.S));
-        sh.recv = sh.alias ? 0 : (sh.stages * stage + ctl - 1024 + 15) & ~15;
-        sh.smem = sh.stages * stage + ctl + (sh.alias ? 0 : recv + 16);
-        return sh;
-    }
-}
-
 template <int S, int E, int CTAS>
 int launch_stream(const LayerStreamParams &p, const StreamShape &sh, cudaStream_t s, int dev)
 {
@@ -707,6 +662,102 @@ int launch_stream(const LayerStreamParams &p, const StreamShape &sh, cudaStream_
     if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return LORA_ERR_CUDA;
     note_launch(kKernLayerStream);
     return LORA_OK;
+}
+
+// Clusters that the device runs at once, with one CTA to an SM; a GPC's odd SMs hold none, so these are fewer
+// than the SMs give (of 148 SMs: 74, 33 and 15).
+struct ClusterFit {
+    int of[4];   // of 1, 2, 4 and 8 CTAs
+    int at_once(int S, int ctas) const
+    {
+        const int w = S / ctas;   // two CTAs to an SM: half the SMs
+        return of[w == 8 ? 3 : w == 4 ? 2 : w == 2 ? 1 : 0];
+    }
+};
+
+template <int S>
+int clusters_at_once()
+{
+    auto kern = layer_stream_kernel<S, 8, 1>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(S);
+    cfg.blockDim = dim3(10 * 32);
+    cfg.dynamicSmemBytes = 210 * 1024;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = S;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess)
+        return 0;   // no clusters
+    return n;
+}
+
+const ClusterFit &cluster_fit(int dev, int n_sms)
+{
+    static std::once_flag once[64];
+    static ClusterFit fit[64];
+    std::call_once(once[dev], [&] {
+        fit[dev] = {{n_sms, clusters_at_once<2>(), clusters_at_once<4>(), clusters_at_once<8>()}};
+    });
+    return fit[dev];
+}
+
+// Tokens per tile: all of them up to 256 (rounded up to the MMA's 16), else equal tiles of at most 256.  Tiles of
+// at most 128, each of at least 96, where twice as many would still find an SM each: the epilogue's work per token
+// is then the longer part (4096 columns, 256 tokens: 1024 rows 23.8 -> 20.1 us, 4608 rows 43.3 -> 30.3; but
+// 14336 -> 4096, 136 tokens 52.4 -> 59.3, and 5120 rows, 192 tokens 35.2 -> 36.7, which the bounds leave out).
+// Clusters: up to 8 CTAs split k, as many as run at once (4096 -> 2048, 64 tokens: 16 clusters of 8 take two
+// rounds, 19.3 us, 16 of 4 one, 13.8), without adapters two to an SM (4096 -> 4096, one token:
+// 8.3 us with 8, 9.3 with 4), with adapters no more than make four CTAs for five SMs (64 tokens: 17.5 us with 4,
+// 18.9 with 8; 14336 outputs: 32.0 with 2, 36.4 with 1), since every CTA more waits for v and for its peers.
+// CTAs per SM: two where half an SM's shared memory holds three stages and half of its tensor memory the
+// accumulator with the adapter terms behind it, else one, as where there is no second CTA to put beside it.
+// Epilogue warps: 16 where the SM has one CTA and more than 64 tokens, since their loads wait on memory most of
+// the time (4096 -> 14336, 256 tokens: 98.9 us with 8, 72.2 with 16; 64 tokens, 14336 -> 4096: 34.6 and 37.3).
+// One CTA alone leaves 16 KB so that a CTA of the shrink fits beside it.
+StreamShape stream_shape(int T, int h, int o, int n_sms, const ClusterFit &fit, bool adapters)
+{
+    StreamShape sh;
+    const int row_tiles = (o + kLM - 1) / kLM;
+    const int halves = (T + kLMaxN / 2 - 1) / (kLMaxN / 2);
+    const bool narrow = T >= halves * 96 && T > kLMaxN / 2 && (int64_t)row_tiles * halves * 2 <= n_sms;
+    sh.NT = narrow ? halves : (T + kLMaxN - 1) / kLMaxN;
+    const int per = (T + sh.NT - 1) / sh.NT;
+    sh.N = (per + 15) & ~15;
+    const int stage = kLWBytes + sh.N * 128;
+    const int64_t tiles = (int64_t)row_tiles * sh.NT;
+    const int nkb = (h + kLK - 1) / kLK;
+    for (int ctas = 2;; --ctas) {
+        sh.E = sh.N <= 32 ? 4 : ctas == 2 || sh.N <= 64 ? 8 : 16;
+        sh.ctas = ctas;
+        const int H = sh.E / 4;
+        sh.S = 1;
+        while (sh.S < 8 && tiles <= fit.at_once(2 * sh.S, ctas) && sh.S * 2 <= nkb &&
+               !(adapters && tiles * sh.S * 5 >= 4ll * n_sms))
+            sh.S *= 2;
+        // S shares cover a whole tile (N, which is more than `per` when there are several)
+        sh.share = ((std::min(sh.N, T) + sh.S - 1) / sh.S + kLBatch - 1) / kLBatch * kLBatch;
+        const int hs = (sh.share / H + kLBatch - 1) / kLBatch * kLBatch;
+        sh.ncols = 32;
+        while (sh.ncols < sh.N + H * hs) sh.ncols *= 2;
+        const int ctl = 1024 + (int)sizeof(LayerStreamCtl) + H * v_bytes(sh.E) + sh.share * 12;
+        const int recv = (sh.S - 1) * sh.share * kLM * 4;
+        const int room = (ctas == 1 ? 210 : 227 / ctas - 1) * 1024 - ctl;
+        // the peers' partial sums beside the ring where that leaves it three stages, else in it
+        sh.alias = (room - recv) / stage < 3;
+        sh.stages = std::min(kLMaxStages, (room - (sh.alias ? 0 : recv)) / stage);
+        if (sh.alias && sh.stages * stage < recv) sh.stages = 0;
+        if (ctas > 1 && (sh.stages < 3 || sh.ncols > 512 / ctas || tiles * sh.S <= n_sms)) continue;
+        sh.stages = std::max(sh.alias ? (recv + stage - 1) / stage : 1, std::min(sh.stages, (nkb + sh.S - 1) / sh.S));
+        sh.recv = sh.alias ? 0 : (sh.stages * stage + ctl - 1024 + 15) & ~15;
+        sh.smem = sh.stages * stage + ctl + (sh.alias ? 0 : recv + 16);
+        return sh;
+    }
 }
 
 template <int E, int CTAS>
@@ -786,7 +837,7 @@ int launch_layer_stream(const lora_table *t, const int32_t *ids, int32_t T, cons
 {
     int dev = 0, n_sms = 0, rc;
     if (device_sms(&dev, &n_sms) != LORA_OK) return LORA_ERR_CUDA;
-    const StreamShape sh = stream_shape(T, t->h, t->o, n_sms, ids != nullptr);
+    const StreamShape sh = stream_shape(T, t->h, t->o, n_sms, cluster_fit(dev, n_sms), ids != nullptr);
     LayerStreamParams p;
     std::memset(&p, 0, sizeof p);
     if ((rc = encode_sw128(&p.tm_x, x, (uint64_t)t->h, (uint64_t)T, (uint64_t)ldx, (uint32_t)sh.N)) != LORA_OK ||
@@ -815,6 +866,7 @@ int launch_layer_stream(const lora_table *t, const int32_t *ids, int32_t T, cons
     p.status = t->d_status;
     p.wait_ns = wait_limit_ns();
     p.inject = (int32_t)(options().inject_stall & 8);
+    if (sh.E == 16) return launch_stream_width<16, 1>(p, sh, s, dev);
     if (sh.E == 4) return sh.ctas == 2 ? launch_stream_width<4, 2>(p, sh, s, dev) : launch_stream_width<4, 1>(p, sh, s, dev);
     return sh.ctas == 2 ? launch_stream_width<8, 2>(p, sh, s, dev) : launch_stream_width<8, 1>(p, sh, s, dev);
 }

@@ -142,6 +142,27 @@ def test_bgmv_layer_sizes(T, h, o):
     m.check(m.bgmv(none), none, "ids of -1")
 
 
+# more than 64 tokens on one CTA of an SM (16 epilogue warps), with k split over 1, 2, 4 and 8 CTAs; from 192
+# tokens on tiles of at most 128; more row tiles than the device runs clusters of 8, and of 4
+@pytest.mark.parametrize("T,h,o", [(65, 64, 72), (67, 128, 136), (79, 256, 200), (101, 520, 264), (128, 64, 4616),
+                                   (191, 136, 128), (192, 136, 128), (250, 264, 72), (253, 640, 136), (287, 72, 64),
+                                   (288, 72, 64), (386, 200, 136), (70, 520, 2048), (5, 520, 2056), (3, 264, 4616)])
+def test_bgmv_layer_wide_epilogues_and_clusters(T, h, o):
+    m = Layer(T, h, o, (128, 5, 16, 64, 40), seed=30, bias=True, act="gelu", mul=True, residual=True, pad=8)
+    ids = m.ids()
+    m.check(m.bgmv(ids), ids, "ids")
+    bad = ids.clone()
+    bad[T // 2:] = 5                               # an adapter that is not there: its rows are left alone
+    m.y.fill_(7.0)
+    m.bgmv(bad)
+    torch.cuda.synchronize()
+    assert (m.y[T // 2:] == 7.0).all()
+    assert L.lora_get_status(m.table.handle) == (L.LORA_ERR_DEVICE_STATUS, L.LORA_STATUS_BAD_ID)
+    none = torch.full((T,), -1, dtype=torch.int32)
+    m.check(m.bgmv(none), none, "ids of -1")
+    m.check(m.bgmv(None), none, "no ids")
+
+
 @pytest.mark.parametrize("act", sorted(ACT))
 @pytest.mark.parametrize("bias,mul,residual", [(False, False, False), (True, False, False), (False, True, False),
                                                (False, False, True), (True, True, True)])

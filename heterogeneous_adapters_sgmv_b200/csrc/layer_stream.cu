@@ -256,25 +256,72 @@ constexpr int kLBatch = 4;                    // tokens an epilogue thread works
 constexpr int v_bytes(int epi_warps) { return epi_warps == 4 ? 2048 : epi_warps == 8 ? 8192 : 4096; }
 static_assert(v_bytes(4) / (LORA_MAX_RANK * 4) >= kLBatch, "a batch of tokens fits");
 
+// One token's term for a rank of 8 LR.  The warp's 32 rows of B are one block, read in LR contiguous pieces of 512
+// bytes: 16 bytes a lane, always the same 8 elements of a row (lane % LR), of row e (32 / LR) + lane / LR in piece e
+// (a lane a row takes 32 sectors a load, and there is next to no L1 beside this much shared memory).  The sums over a
+// row's LR lanes are formed while the rows are dealt out, so that lane = row again.
+template <int LR>
+__device__ __forceinline__ float expand_block(const void *B, int64_t n, int rows, const float *v)
+{
+    const int lane = threadIdx.x & 31;
+    const uint16_t *src = static_cast<const uint16_t *>(B) + (n - lane) * (8 * LR) + lane * 8;
+    const float4 p = *reinterpret_cast<const float4 *>(v + lane % LR * 8);
+    const float4 q = *reinterpret_cast<const float4 *>(v + lane % LR * 8 + 4);
+    float s[LR];
+#pragma unroll
+    for (int e = 0; e < LR; ++e) {
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (e * (32 / LR) + lane / LR < rows) w = *reinterpret_cast<const uint4 *>(src + e * 256);
+        float s0 = bf16_lo(w.x) * p.x, s1 = bf16_hi(w.x) * p.y;
+        s0 = fmaf(bf16_lo(w.y), p.z, s0);
+        s1 = fmaf(bf16_hi(w.y), p.w, s1);
+        s0 = fmaf(bf16_lo(w.z), q.x, s0);
+        s1 = fmaf(bf16_hi(w.z), q.y, s1);
+        s0 = fmaf(bf16_lo(w.w), q.z, s0);
+        s1 = fmaf(bf16_hi(w.w), q.w, s1);
+        s[e] = s0 + s1;
+    }
+#pragma unroll
+    for (int g = LR / 2; g > 0; g /= 2)
+#pragma unroll
+        for (int e = 0; e < g; ++e) {
+            const bool up = lane & g;
+            const float give = up ? s[e] : s[e + g];
+            s[e] = (up ? s[e + g] : s[e]) + __shfl_xor_sync(0xffffffffu, give, g);
+        }
+    return __shfl_sync(0xffffffffu, s[0], lane % (32 / LR) * LR + lane / (32 / LR));
+}
+
 // The adapter terms of one thread's output column n, a batch of tokens at a time:
 //   d[j] = sum_k B_j[n, k] v_j[k].
 // Rows of a rank that is a multiple of 8 are 16-byte aligned and read NP pieces of 8 a step, the step's
 // loads together (under a saturated memory system a load takes 2 to 4 us) and the first step's before v is
-// there; other rows are read element by element, the batch's together.
-template <int NP>
+// there.
+// ANY: the table may hold other ranks.  Rows of a rank that is no multiple of 8 are read by the aligned pieces that
+// they lie in (the matrix starts on 16 bytes and, o being a multiple of 8, ends there, so no piece leaves it), and
+// what belongs to their neighbours is passed over (4096 -> 14336, 64 tokens of rank 60: 461 us element by element,
+// 117 so; of rank 12: 65.7 and 46.2).  Ranks of 64 and 128 go by expand_block (92.5 -> 76.1 and 170.5 -> 107.4 us).  A
+// kernel of its own, since the registers that this takes cost the others (rank 16: 31.6 us without, 41.9 with).
+template <int NP, bool ANY>
 struct ExpandRows {
     static constexpr int NB = kLBatch;
     const int32_t *rank;        // per token; <= 0: none
     const void *const *B;
     int64_t n;
     bool col_ok;
+    int rows;                   // rows of W in this warp
     int end;                    // tokens of this thread: the batches end here
     uint4 b[NB][NP];            // the step at hand
 
+    // ranks whose rows are read 16 bytes a lane, a lane a row
+    static __device__ __forceinline__ bool in_steps(int r)
+    {
+        return r > 0 && (!ANY || ((r & 7) == 0 && r != 64 && r != 128));
+    }
     __device__ __forceinline__ int even(int i) const
     {
         const int r = i < end && col_ok ? rank[i] : 0;
-        return r > 0 && (r & 7) == 0 ? r : 0;
+        return in_steps(r) ? r : 0;
     }
     __device__ __forceinline__ void load(int i, int k)
     {
@@ -293,7 +340,7 @@ struct ExpandRows {
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
             const int r = i + j < end ? rank[i + j] : 0;
-            if ((r & 7) == 0) most = max(most, r);
+            if (in_steps(r)) most = max(most, r);
         }
         return most;
     }
@@ -323,32 +370,52 @@ struct ExpandRows {
             }
             if (k + 8 * NP < most) load(i, k + 8 * NP);
         }
-        int odd[NB], longest = 0;
+        if constexpr (ANY) others(i, v, ldv, d);
+        load(i + NB, 0);
+    }
+    // what is not in_steps of the batch at i
+    __device__ __forceinline__ void others(int i, const float *v, int ldv, float (&d)[NB]) const
+    {
+#pragma unroll 1
+        for (int j = 0; j < NB; ++j) {
+            const int r = i + j < end && rows > 0 ? rank[i + j] : 0;
+            if (r != 64 && r != 128) continue;
+            const float t = r == 64 ? expand_block<8>(B[i + j], n, rows, v + j * ldv)
+                                    : expand_block<16>(B[i + j], n, rows, v + j * ldv);
+#pragma unroll
+            for (int u = 0; u < NB; ++u) d[u] += u == j ? t : 0.f;
+        }
+        // a row starts `off` elements into an aligned piece
+        int odd[NB], off[NB], longest = 0;
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
             const int r = i + j < end && col_ok ? rank[i + j] : 0;
-            odd[j] = r & 7 ? r : 0;
-            longest = max(longest, odd[j]);
+            odd[j] = r > 0 && (r & 7) ? r : 0;
+            off[j] = (int)(n * odd[j]) & 7;
+            longest = max(longest, off[j] + odd[j]);
         }
-        for (int k = 0; k < longest; k += 4) {
-            uint16_t w[NB][4];
+        for (int k = 0; k < longest; k += 8) {
+            uint4 w[NB];
 #pragma unroll
             for (int j = 0; j < NB; ++j)
+                if (k < off[j] + odd[j])
+                    w[j] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(B[i + j]) + n * odd[j] -
+                                                            off[j] + k);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    w[j][e] = k + e < odd[j] ? static_cast<const uint16_t *>(B[i + j])[n * odd[j] + k + e] : (uint16_t)0;
+            for (int j = 0; j < NB; ++j) {
+                const uint32_t u[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+                const int at = k - off[j];
 #pragma unroll
-            for (int j = 0; j < NB; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (k + e < odd[j]) d[j] = fmaf(bf16_f(w[j][e]), v[j * ldv + k + e], d[j]);
+                for (int q = 0; q < 8; ++q)
+                    if ((uint32_t)(at + q) < (uint32_t)odd[j])
+                        d[j] = fmaf(q & 1 ? bf16_hi(u[q / 2]) : bf16_lo(u[q / 2]), v[j * ldv + at + q], d[j]);
+            }
         }
-        load(i + NB, 0);
     }
 };
 
 // S CTAs of a cluster split the k axis; E epilogue warps (see stream_shape); CTAS to an SM.
-template <int S, int E, int CTAS>
+template <int S, int E, int CTAS, bool ANY>
 __global__ void __launch_bounds__(E * 32 + 64, CTAS) layer_stream_kernel(const __grid_constant__ LayerStreamParams p)
 {
     // 16-byte pieces of B_i's rows in registers, for each token of a batch: four where there are registers for
@@ -507,11 +574,12 @@ __global__ void __launch_bounds__(E * 32 + 64, CTAS) layer_stream_kernel(const _
         }
         // While W streams: bias and adapter term of every output, kept in tensor memory behind the
         // accumulator.
-        ExpandRows<NP> ex;
+        ExpandRows<NP, ANY> ex;
         ex.rank = tok_rank;
         ex.B = tok_B;
         ex.n = n;
         ex.col_ok = col_ok;
+        ex.rows = rows_left;
         ex.end = i1;
         ex.load(i0, 0);
         float *vs = reinterpret_cast<float *>(v_buf + part * v_bytes(E));
@@ -628,10 +696,10 @@ struct StreamShape {
     int N, NT, S, E, ctas, stages, share, ncols, recv, alias, smem;
 };
 
-template <int S, int E, int CTAS>
+template <int S, int E, int CTAS, bool ANY>
 int launch_stream(const LayerStreamParams &p, const StreamShape &sh, cudaStream_t s, int dev)
 {
-    auto kern = layer_stream_kernel<S, E, CTAS>;
+    auto kern = layer_stream_kernel<S, E, CTAS, ANY>;
     static std::once_flag once[64];
     static cudaError_t attr_rc[64];
     std::call_once(once[dev], [&] {
@@ -678,7 +746,7 @@ struct ClusterFit {
 template <int S>
 int clusters_at_once()
 {
-    auto kern = layer_stream_kernel<S, 8, 1>;
+    auto kern = layer_stream_kernel<S, 8, 1, false>;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(S);
     cfg.blockDim = dim3(10 * 32);
@@ -760,15 +828,24 @@ StreamShape stream_shape(int T, int h, int o, int n_sms, const ClusterFit &fit, 
     }
 }
 
-template <int E, int CTAS>
+template <int E, int CTAS, bool ANY>
 int launch_stream_width(const LayerStreamParams &p, const StreamShape &sh, cudaStream_t s, int dev)
 {
     switch (sh.S) {
-    case 8: return launch_stream<8, E, CTAS>(p, sh, s, dev);
-    case 4: return launch_stream<4, E, CTAS>(p, sh, s, dev);
-    case 2: return launch_stream<2, E, CTAS>(p, sh, s, dev);
-    default: return launch_stream<1, E, CTAS>(p, sh, s, dev);
+    case 8: return launch_stream<8, E, CTAS, ANY>(p, sh, s, dev);
+    case 4: return launch_stream<4, E, CTAS, ANY>(p, sh, s, dev);
+    case 2: return launch_stream<2, E, CTAS, ANY>(p, sh, s, dev);
+    default: return launch_stream<1, E, CTAS, ANY>(p, sh, s, dev);
     }
+}
+
+template <bool ANY>
+int launch_stream_shape(const LayerStreamParams &p, const StreamShape &sh, cudaStream_t s, int dev)
+{
+    if (sh.E == 16) return launch_stream_width<16, 1, ANY>(p, sh, s, dev);
+    if (sh.E == 8)
+        return sh.ctas == 2 ? launch_stream_width<8, 2, ANY>(p, sh, s, dev) : launch_stream_width<8, 1, ANY>(p, sh, s, dev);
+    return sh.ctas == 2 ? launch_stream_width<4, 2, ANY>(p, sh, s, dev) : launch_stream_width<4, 1, ANY>(p, sh, s, dev);
 }
 
 int device_sms(int *dev, int *n_sms)
@@ -866,9 +943,10 @@ int launch_layer_stream(const lora_table *t, const int32_t *ids, int32_t T, cons
     p.status = t->d_status;
     p.wait_ns = wait_limit_ns();
     p.inject = (int32_t)(options().inject_stall & 8);
-    if (sh.E == 16) return launch_stream_width<16, 1>(p, sh, s, dev);
-    if (sh.E == 4) return sh.ctas == 2 ? launch_stream_width<4, 2>(p, sh, s, dev) : launch_stream_width<4, 1>(p, sh, s, dev);
-    return sh.ctas == 2 ? launch_stream_width<8, 2>(p, sh, s, dev) : launch_stream_width<8, 1>(p, sh, s, dev);
+    // the table's ranks: all multiples of 8, none above 64 and some below (a table of 64 alone is better off with
+    // its block reads, 92.5 -> 76.1 us; one of 8 to 64 is not, 51.2 -> 58.2; 4096 -> 14336, 64 tokens)
+    const bool plain = !ids || (t->ranks_of_8 && t->max_rank <= 64 && t->min_rank < 64);
+    return plain ? launch_stream_shape<false>(p, sh, s, dev) : launch_stream_shape<true>(p, sh, s, dev);
 }
 
 }  // namespace lora

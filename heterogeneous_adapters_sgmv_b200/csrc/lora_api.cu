@@ -294,6 +294,7 @@ int lora_table_create(lora_table **out, int32_t n, int32_t h, int32_t o, int32_t
     t->o = o;
     t->dtype = dtype;
     t->max_rank = max_rank;
+    t->ranks_of_8 = std::all_of(ranks, ranks + n, [](int32_t r) { return r % 8 == 0; });
     t->min_rank = min_rank;
     t->d_desc = nullptr;
     t->d_status = nullptr;

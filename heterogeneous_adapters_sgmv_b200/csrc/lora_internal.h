@@ -160,4 +160,5 @@ struct lora_table {
     // three-stage form: LORA_SIGMA_* and the per-adapter Sigma_i pointers (device, fp32)
     int32_t sigma_kind;
     std::vector<const float *> sigma;
+    bool ranks_of_8;   // every rank is a multiple of 8
 };

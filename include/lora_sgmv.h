@@ -240,9 +240,8 @@ int lora_bgmv_merged(const lora_table *table, const int32_t *d_ids, const float 
  * of the table's type, 16-byte aligned, ld.. >= o and a multiple of 8.  mul is the other half of a
  * gated MLP (its up projection, when this call is the gate with LORA_ACT_SILU).  residual or mul
  * may be the y slice itself (same address and row stride: an update in place); any other overlap
- * of y with x, mul or residual is LORA_ERR_INVALID_ARG.  bias and W are weights: like a table's
- * A_i and B_i they may be read ahead of the stream's earlier work, so a call of this library that
- * is still in flight must not be writing them.
+ * of y with x, mul or residual is LORA_ERR_INVALID_ARG.  Only the table and its A_i and B_i are taken as
+ * unchanging; everything else, W and bias included, may be written by the stream's work just before.
  * The layer and norm calls want the table's device to be the current one (LORA_ERR_INVALID_ARG).  A
  * workspace serves one call at a time: calls that may overlap on the GPU (other streams, captured
  * graphs replayed side by side) need one each. */

@@ -27,3 +27,11 @@ def test_gemm_issuer_reads_a_stage_before_it_gives_it_back():
     base, adapters = [m.start() for m in re.finditer(r"umma_commit_pair\(empty0", loop)]
     assert loop.index("ctl.last[") < base
     assert loop.index("ctl.lo[") < adapters and loop.index("ctl.hi[") < adapters
+
+
+def test_weight_pass_waits_before_it_reads_anything():
+    """Without a shrink in front (`early` is 0) the producer's wait for the stream's earlier work comes before
+    its first load, of W as of x: W may have been written by the kernel before."""
+    src = part("layer_stream.cu", "---- producer", "---- MMA issuer")
+    wait = src.index("if (!p.early) pdl_wait();")
+    assert src.count("pdl_wait()") == 1 and wait < src.index("tma_load_2d(") and wait < src.index("&p.tm_w")

@@ -782,6 +782,13 @@ int layer_v_parts(int32_t T, int32_t h)
     return std::min(kVParts, std::max(1, h / (kShrinkK * kShrinkWarps * 4)));
 }
 
+// Batches above kLayerPartTokens need fewer rows a token; a workspace made for one serves the smaller ones too.
+int64_t layer_v_rows(int32_t T, int32_t h)
+{
+    const int32_t in_parts = std::min(T, kLayerPartTokens);
+    return std::max<int64_t>(T, (int64_t)layer_v_parts(in_parts, h) * in_parts);
+}
+
 int launch_layer_shrink(const lora_table *t, const int32_t *ids, int32_t T, const void *x, int64_t ldx, float *v,
                         int32_t ldv, cudaStream_t s)
 {

@@ -108,7 +108,7 @@ WsLayout ws_layout(const lora_table *t, int32_t T)
     off += 256;
     w.total = off;
     w.layer = off;
-    w.layer_total = off + up256((size_t)layer_v_parts(T, t->h) * T * ldv_of(t) * sizeof(float));
+    w.layer_total = off + up256((size_t)layer_v_rows(T, t->h) * ldv_of(t) * sizeof(float));
     return w;
 }
 

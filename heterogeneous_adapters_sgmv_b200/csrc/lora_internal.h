@@ -118,6 +118,7 @@ int launch_layer_gemm(const lora_table *t, const lora_segments *seg, const void 
 // is not null.
 constexpr int32_t kLayerPartTokens = 512;   // batches up to this may have v in several parts
 int layer_v_parts(int32_t T, int32_t h);
+int64_t layer_v_rows(int32_t T, int32_t h);   // room for v of T tokens and of any fewer, in rows of ldv
 int launch_layer_shrink(const lora_table *t, const int32_t *ids, int32_t T, const void *x, int64_t ldx, float *v,
                         int32_t ldv, cudaStream_t s);
 int launch_layer_stream(const lora_table *t, const int32_t *ids, int32_t T, const void *x, int64_t ldx, const void *W,

@@ -130,7 +130,8 @@ int lora_table_info(const lora_table *table, int32_t *n_adapters, int32_t *h_in,
                     int32_t *h_out, int32_t *max_rank, int32_t *dtype);
 
 /* Bytes of device workspace that lora_sgmv, lora_bgmv and the layer calls need for T tokens (a multiple of
- * 256; 0 is never returned). */
+ * 256; 0 is never returned).  It never falls as T grows: a workspace for the largest batch serves every
+ * smaller one. */
 size_t lora_workspace_bytes(const lora_table *table, int32_t T);
 
 /* Segment bookkeeping (SGMV grouping): a stable sort of the tokens by adapter id.

@@ -85,7 +85,7 @@ inline int ldv_of(const lora_table *t) { return (t->max_rank + 3) & ~3; }
 
 struct WsLayout {
     size_t v, perm, seg_ptr, seg_adapter, num_segs, tile_ctr, total;
-    size_t layer, layer_total;   // lora_bgmv_layer's intermediate, behind the areas of the other calls
+    size_t layer_total;   // with room for lora_bgmv_layer's intermediate, which takes the place of all of these
 };
 
 WsLayout ws_layout(const lora_table *t, int32_t T)
@@ -107,8 +107,10 @@ WsLayout ws_layout(const lora_table *t, int32_t T)
     w.tile_ctr = off + 128;   // the tcgen05 expand's tile counter, in the same 256-byte block
     off += 256;
     w.total = off;
-    w.layer = off;
-    w.layer_total = off + up256((size_t)layer_v_rows(T, t->h) * ldv_of(t) * sizeof(float));
+    // a workspace serves one call at a time, and none leaves anything in it for the next
+    w.layer_total = off;
+    if (t->dtype == LORA_BF16)
+        w.layer_total = std::max(off, up256((size_t)layer_v_rows(T, t->h) * ldv_of(t) * sizeof(float)));
     return w;
 }
 
@@ -764,7 +766,7 @@ int lora_bgmv_layer(const lora_table *t, const int32_t *d_ids, int32_t T, const 
     }
     float *v = nullptr;
     if (d_ids) {
-        v = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.layer);
+        v = static_cast<float *>(ws);
         if ((rc = launch_layer_shrink(t, d_ids, T, x, ldx, v, ldv_of(t), s)) != LORA_OK) return rc;
     }
     return launch_layer_stream(t, d_ids, T, x, ldx, W, ldw, epi ? epi : &none, y, ldy, y_off, v, ldv_of(t), s);

@@ -23,3 +23,21 @@ def test_workspace_grows_with_the_batch(h, rank):
     sizes = [need(t, T) for T in TOKENS]
     assert all(s > 0 and s % 256 == 0 for s in sizes)
     assert sizes == sorted(sizes)
+
+
+def plain(T, n, ldv, tcgen05):
+    """What the calls without a layer need: the intermediate (fp32, or hi and lo of 64 columns), sorted
+    tokens, segment bounds and adapters, and one block of counters, each rounded up to 256 bytes."""
+    up = lambda b: (b + 255) // 256 * 256
+    return (up(max(T * ldv * 4, T * 256 if tcgen05 else 0)) + up(4 * T) + up(4 * (n + 1)) + up(4 * n) + 256)
+
+
+@pytest.mark.parametrize("T", [0, 1, 64, 300, 512, 513, 1024, 2048, 5000])
+def test_workspace_grows_only_where_the_layer_call_needs_it(T):
+    """fp32 tables have no layer call; large batches keep its intermediate in one part, where that of the other
+    calls lies."""
+    assert need(table(h=4096, dtype=L.LORA_F32, d_tmaps_pfA=None), T) == plain(T, 4, 16, False)
+    for h, rank, tcgen05 in ((4096, 16, True), (4096, 64, True), (4096, 128, False), (256, 128, False)):
+        got = need(table(h=h, max_rank=rank, d_tmaps_pfA=P if tcgen05 else None), T)
+        rows = T if h < 2048 else max(T, 4 * min(T, 512))
+        assert got == max(plain(T, 4, rank, tcgen05), (rows * rank * 4 + 255) // 256 * 256)

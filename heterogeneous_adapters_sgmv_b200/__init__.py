@@ -177,7 +177,9 @@ def _ptr(obj) -> Optional[int]:
     try:
         return obj.data_ptr()
     except AttributeError:
-        return int(obj)
+        if isinstance(obj, int):
+            return obj
+        raise
 
 
 _torch_c = None

@@ -172,8 +172,8 @@ def _load():
 
 
 def _ptr(obj) -> Optional[int]:
-    if obj is None:
-        return None
+    if obj is None or type(obj) is int:
+        return obj
     try:
         return obj.data_ptr()
     except AttributeError:

@@ -1,5 +1,6 @@
 """How the binding takes pointers: tensors and whole numbers, and nothing that merely converts to one."""
 import ctypes
+import timeit
 
 import numpy as np
 import pytest
@@ -19,3 +20,11 @@ def test_pointer_of_tensors_and_numbers():
 def test_pointer_of_anything_else_is_refused(obj):
     with pytest.raises(AttributeError):
         L._ptr(obj)
+
+
+def test_pointer_of_a_number_costs_no_more_than_that_of_a_tensor():
+    """A raw address needs no attribute lookup that fails first (ten times a tensor's cost; the bound is three)."""
+    t, best = torch.zeros(4), {}
+    for k, obj in (("number", 1 << 40), ("tensor", t)):
+        best[k] = min(timeit.repeat(lambda: L._ptr(obj), number=5000, repeat=15))
+    assert best["number"] < 3 * best["tensor"], best

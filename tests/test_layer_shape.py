@@ -86,3 +86,18 @@ def test_clusters_never_wait_for_each_others_tensor_memory(shape):
         return max([0] + [cols + worst(room - smem - 1024) for cols, smem in least.items() if smem + 1024 <= room])
 
     assert worst(228 * 1024) <= 512
+
+
+def test_gpu_sizes_reach_the_forms_they_are_for(shape):
+    """The sizes of test_bgmv_layer_long_rings, with and without ids."""
+    from tests.test_gpu_layer_forms import ROUNDS
+    seen, parts = set(), set()
+    for T, h, o in ROUNDS:
+        s = shape(T, h, o)
+        if -(-h // 64) // s.S > 2 * s.stages:
+            seen.add((s.S, s.ctas, bool(s.alias)))
+        if T > 1:
+            parts.add(min(4, max(1, h // 1024)) if T <= 512 else 1)
+    assert {(1, 1, False), (1, 2, False), (2, 1, False), (4, 1, False), (8, 1, False), (2, 1, True), (2, 2, True),
+            (4, 2, True), (8, 2, True), (8, 2, False)} <= seen
+    assert parts == {1, 2, 3, 4}

@@ -486,7 +486,7 @@ constexpr int gemm_smem(int bn, int stages, int tiles)
 constexpr int gemm_stages(int bn, int tiles) { return bn == 256 ? (tiles == 2 ? 5 : 6) : (tiles == 2 ? 3 : 4); }
 static_assert(gemm_smem(256, 6, 1) <= 227 * 1024 && gemm_smem(256, 5, 2) <= 227 * 1024, "shared memory");
 static_assert(gemm_smem(128, 4, 1) <= 227 * 1024 && gemm_smem(128, 3, 2) <= 227 * 1024, "shared memory");
-// no other pair or cluster that takes tensor memory fits beside a CTA (kClusterSmem in layer_shape.h says why)
+// no other pair or cluster that takes tensor memory fits beside a CTA (kColumnSmem in layer_shape.h says why)
 static_assert(gemm_smem(256, 5, 2) >= 200 * 1024 && gemm_smem(128, 3, 2) >= 200 * 1024, "alone on its SM");
 
 template <int BN, int TILES>

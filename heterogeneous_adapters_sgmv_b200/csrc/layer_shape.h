@@ -30,13 +30,13 @@ constexpr int kLBatch = 4;                    // tokens an epilogue thread works
 constexpr int v_bytes(int epi_warps) { return epi_warps == 4 ? 2048 : epi_warps == 8 ? 8192 : 4096; }
 static_assert(v_bytes(4) / (LORA_MAX_RANK * 4) >= kLBatch, "a batch of tokens fits");
 
-// Least shared memory of a CTA in a cluster, by CTAs to an SM.  Such a CTA holds its tensor memory until its peers
-// have sent their sums, and they may still be waiting for theirs: if the CTAs that fit an SM could ask for more than its
-// 512 columns, two clusters (of one launch, or of two streams) could each hold what the other waits for, for good.
-// So they are kept apart by shared memory (228 KB to an SM): one with up to 512 columns leaves no room for any other
-// cluster that takes tensor memory (the least is a CTA of the long segments' shrink, 97 KB and 64 columns), and of
-// those with up to 256 columns there are two, or one and one of the shrink.  What runs without a cluster ends by itself.
-constexpr int kClusterSmem[3] = {0, 200 * 1024, 100 * 1024};
+// Least shared memory of a CTA in a cluster, a column of tensor memory (64 at least).  Such a CTA holds its tensor
+// memory until its peers have sent their sums, and they may still be waiting for theirs: if the CTAs that fit an SM
+// could ask for more than its 512 columns, two clusters (of one launch, or of two streams) could each hold what the
+// other waits for, for good.  An SM has 228 KB, of which a CTA takes 1 KB beside its own: what fits it then has at most
+// 571 columns, in steps of 64, so 512.  The other clusters that take tensor memory take more (the long segments' shrink
+// 97 KB for 64 columns; lora_sgmv_layer's pairs fill an SM), and what runs without a cluster ends by itself.
+constexpr int kColumnSmem = 408;
 
 struct StreamShape {
     int N, NT, S, E, ctas, stages, share, ncols, recv, alias, smem;
@@ -102,7 +102,7 @@ StreamShape stream_shape(int T, int h, int o, int n_sms, const ClusterFit &fit, 
         sh.stages = std::max(sh.alias ? (recv + stage - 1) / stage : 1, std::min(sh.stages, (nkb + sh.S - 1) / sh.S));
         sh.recv = sh.alias ? 0 : (sh.stages * stage + ctl - 1024 + 15) & ~15;
         sh.smem = sh.stages * stage + ctl + (sh.alias ? 0 : recv + 16);
-        if (sh.S > 1) sh.smem = std::max(sh.smem, kClusterSmem[ctas]);
+        if (sh.S > 1) sh.smem = std::max(sh.smem, std::max(64, sh.ncols) * kColumnSmem);
         return sh;
     }
 }

@@ -457,8 +457,13 @@ __global__ void __launch_bounds__(E * 32 + 64, CTAS) layer_stream_kernel(const _
         const bool one = elect_one();
         const int pre = min(nkb, p.stages);
         // Behind the shrink, whose CTAs have all waited for what came earlier, x and W are final.  Without it
-        // nothing is, W included: a kernel right before this one may have written it.
-        if (!p.early) pdl_wait();
+        // nothing is, W included (a kernel right before this one may have written it), and what W holds now is
+        // only asked into L2, where a later write changes it.
+        if (!p.early) {
+            if (one)
+                for (int kb = 0; kb < pre; ++kb) tma_prefetch_2d(&p.tm_w, (kb0 + kb) * kLK, row0);
+            pdl_wait();
+        }
         if (one)
             for (int kb = 0; kb < pre; ++kb) {
                 mbar_arrive_expect_tx(full0 + kb * 8, (uint32_t)stage_bytes);

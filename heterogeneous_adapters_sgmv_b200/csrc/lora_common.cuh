@@ -249,6 +249,12 @@ __device__ __forceinline__ void tma_store_2d_hint(const void *tmap, uint32_t src
                  : "memory");
 }
 
+// Hint: bring box {c0, c1} of `tmap` into L2.
+__device__ __forceinline__ void tma_prefetch_2d(const void *tmap, int32_t c0, int32_t c1)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(tmap), "r"(c0), "r"(c1) : "memory");
+}
+
 // Hint: bring a 128-byte line into L2.
 __device__ __forceinline__ void prefetch_l2(const void *p)
 {

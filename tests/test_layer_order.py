@@ -33,5 +33,7 @@ def test_weight_pass_waits_before_it_reads_anything():
     """Without a shrink in front (`early` is 0) the producer's wait for the stream's earlier work comes before
     its first load, of W as of x: W may have been written by the kernel before."""
     src = part("layer_stream.cu", "---- producer", "---- MMA issuer")
-    wait = src.index("if (!p.early) pdl_wait();")
-    assert src.count("pdl_wait()") == 1 and wait < src.index("tma_load_2d(") and wait < src.index("&p.tm_w")
+    assert src.count("pdl_wait()") == 1 and src.index("pdl_wait()") < src.index("tma_load_2d(")
+    before = src[:src.index("pdl_wait()")]
+    # what stands before it asks L2, and changes nothing
+    assert "if (!p.early)" in before and before.count("&p.tm_w") == before.count("tma_prefetch_2d(") == 1

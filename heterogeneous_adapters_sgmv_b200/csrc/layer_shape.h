@@ -65,7 +65,9 @@ struct ClusterFit {
 // accumulator with the adapter terms behind it, else one, as where there is no second CTA to put beside it.
 // Epilogue warps: 16 where the SM has one CTA and more than 64 tokens, since their loads wait on memory most of
 // the time (4096 -> 14336, 256 tokens: 98.9 us with 8, 72.2 with 16; 64 tokens, 14336 -> 4096: 34.6 and 37.3).
-// One CTA alone leaves 16 KB so that a CTA of the shrink fits beside it.
+// One CTA alone of 4 epilogue warps leaves 16 KB so that a CTA of the shrink (256 threads of 118 registers) fits
+// beside it; with more warps the registers do not, and it takes all (4096 -> 14336, 256 tokens: 67.6 -> 66.5 us; 512
+// tokens: 126.6 -> 124.7; 128 tokens: 41.9 -> 41.5).
 StreamShape stream_shape(int T, int h, int o, int n_sms, const ClusterFit &fit, bool adapters)
 {
     StreamShape sh;
@@ -93,7 +95,7 @@ StreamShape stream_shape(int T, int h, int o, int n_sms, const ClusterFit &fit, 
         while (sh.ncols < sh.N + H * hs) sh.ncols *= 2;
         const int ctl = 1024 + (int)sizeof(LayerStreamCtl) + H * v_bytes(sh.E) + sh.share * 12;
         const int recv = (sh.S - 1) * sh.share * kLM * 4;
-        const int room = (ctas == 1 ? 210 : 227 / ctas - 1) * 1024 - ctl;
+        const int room = (ctas == 1 ? (sh.E == 4 ? 210 : 226) : 227 / ctas - 1) * 1024 - ctl;
         // the peers' partial sums beside the ring where that leaves it three stages, else in it
         sh.alias = (room - recv) / stage < 3;
         sh.stages = std::min(kLMaxStages, (room - (sh.alias ? 0 : recv)) / stage);

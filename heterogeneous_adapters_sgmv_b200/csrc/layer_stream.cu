@@ -799,8 +799,8 @@ int launch_layer_shrink(const lora_table *t, const int32_t *ids, int32_t T, cons
 {
     int dev = 0, n_sms = 0;
     if (device_sms(&dev, &n_sms) != LORA_OK) return LORA_ERR_CUDA;
-    // The pass over W wants all of an SM's shared memory; with the same split of the SM's memory here its
-    // CTAs can join this kernel's on an SM instead of waiting for the SM to empty.
+    // With the same split of the SM's shared memory as the pass over W, whose CTAs can then join this kernel's on an
+    // SM where registers allow (4 epilogue warps, or two CTAs to an SM) instead of waiting for the SM to empty.
     static std::once_flag once[64];
     std::call_once(once[dev], [] {
         cudaFuncSetAttribute(layer_shrink_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,

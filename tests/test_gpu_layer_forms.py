@@ -58,7 +58,8 @@ def test_activations_keep_their_relative_accuracy_in_the_lower_tail(act):
 # test_layer_shape.py holds that these sizes do so.
 ROUNDS = [(1, 1032, 15240), (120, 648, 9480), (40, 520, 19208), (40, 2120, 4616), (390, 1352, 1032), (512, 840, 2312),
           (70, 840, 9480), (40, 3784, 2056), (1030, 2248, 136), (1, 2760, 5128), (63, 1736, 5128), (129, 3528, 72),
-          (40, 3528, 2312), (63, 3528, 2312), (33, 4104, 136), (256, 3080, 2056), (512, 1160, 2312)]
+          (40, 3528, 2312), (63, 3528, 2312), (33, 4104, 136), (256, 3080, 2056), (512, 1160, 2312),
+          (129, 4616, 72), (40, 4360, 2056)]
 
 
 @pytest.mark.parametrize("ranks", [(16, 40, 8), (128, 5, 64)])

@@ -49,6 +49,7 @@ LORA_GATE_NONE = 0
 LORA_GATE_ADAPTER = 1
 LORA_GATE_TOKEN = 2
 LORA_MAX_NORM_WIDTH = 16384
+LORA_MAX_LAYER_TOKENS = 1 << 30
 
 EXPORTS = (
     "lora_table_create", "lora_table_destroy", "lora_table_info", "lora_workspace_bytes",

@@ -722,7 +722,7 @@ int lora_sgmv_layer(const lora_table *t, const lora_segments *seg, const void *x
     if ((rc = check_segments(seg))) return rc;
     if ((rc = check_io(t, x, ldx, y, ldy, y_off, true, true))) return rc;
     if (!W || ldw < t->h) return LORA_ERR_INVALID_ARG;
-    if (!al16(W) || ldw % 8) return LORA_ERR_UNSUPPORTED;
+    if (!al16(W) || ldw % 8 || seg->T > LORA_MAX_LAYER_TOKENS) return LORA_ERR_UNSUPPORTED;
     if (!prefill_supported(t) || seg->perm != nullptr) return LORA_ERR_UNSUPPORTED;
     if ((rc = check_epilogue(epi, t, seg->T, x, ldx, y, ldy, y_off))) return rc;
     if (seg->T == 0) return LORA_OK;
@@ -747,7 +747,7 @@ int lora_bgmv_layer(const lora_table *t, const int32_t *d_ids, int32_t T, const 
     if (T < 0) return LORA_ERR_INVALID_ARG;
     if ((rc = check_io(t, x, ldx, y, ldy, y_off, true, true))) return rc;
     if (!W || ldw < t->h) return LORA_ERR_INVALID_ARG;
-    if (!al16(W) || ldw % 8) return LORA_ERR_UNSUPPORTED;
+    if (!al16(W) || ldw % 8 || T > LORA_MAX_LAYER_TOKENS) return LORA_ERR_UNSUPPORTED;
     if (t->dtype != LORA_BF16 || t->sigma_kind != LORA_SIGMA_NONE) return LORA_ERR_UNSUPPORTED;
     if ((rc = check_epilogue(epi, t, T, x, ldx, y, ldy, y_off))) return rc;
     if (T == 0) return LORA_OK;

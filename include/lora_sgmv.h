@@ -245,7 +245,9 @@ int lora_bgmv_merged(const lora_table *table, const int32_t *d_ids, const float 
  * unchanging; everything else, W and bias included, may be written by the stream's work just before.
  * The layer and norm calls want the table's device to be the current one (LORA_ERR_INVALID_ARG).  A
  * workspace serves one call at a time: calls that may overlap on the GPU (other streams, captured
- * graphs replayed side by side) need one each. */
+ * graphs replayed side by side) need one each.  T is at most LORA_MAX_LAYER_TOKENS in the layer calls (else
+ * LORA_ERR_UNSUPPORTED). */
+#define LORA_MAX_LAYER_TOKENS (1 << 30)
 #define LORA_ACT_NONE 0
 #define LORA_ACT_RELU 1      /* max(z, 0)                                                        */
 #define LORA_ACT_GELU 2      /* z Phi(z), Phi the normal distribution function                   */

@@ -12,7 +12,7 @@
 // depend on).  Where there are many rows the blocks are persistent (ring_norm_kernel): a warp of its own brings the
 // operands of the rows to come, the weights of each row's adapter among them, into a ring in shared memory by bulk
 // copies, and weights that serve all rows once, so that neither a global load's latency nor the issue of the copies
-// lies between a row's sums.  4096 rows of 4096 bf16: before 14.8 us, after (with the next norm) 31.3, 80 and 82 %
+// lies between a row's sums.  4096 rows of 4096 bf16: before 14.8 us, after (with the next norm) 31.3, 69 and 82 %
 // of the copy bandwidth; a block a row takes 18.0 and 43.9.
 // The variance of a layer norm is taken from the centred values in a second sum over the registers, not from the
 // difference of two large sums.  h is computed from the unrounded r, so that a fused call adds no rounding of its
@@ -472,7 +472,8 @@ int launch_kernel(const NormParams &p, cudaStream_t s)
     return LORA_OK;
 }
 
-// Rows per SM from which a ring pays (4096 wide, bf16, a block a row against the ring): before a block, which has
+// Rows per SM from which a ring pays, measured 4096 wide in bf16 only and taken for all widths and types (a block a
+// row against the ring): before a block, which has
 // one operand, 8 rows an SM 6.1 and 6.5 us, 12 rows 9.35 and 8.4; after it, 1 row 3.0 and 3.5 us, 4 rows 8.8 and
 // 8.4, 8 rows 15.5 and 12.6.
 constexpr int ring_rows_per_sm(bool after) { return after ? 4 : 12; }

@@ -66,7 +66,8 @@ struct ClusterFit {
 // Epilogue warps: 16 where the SM has one CTA and more than 64 tokens, since their loads wait on memory most of
 // the time (4096 -> 14336, 256 tokens: 98.9 us with 8, 72.2 with 16; 64 tokens, 14336 -> 4096: 34.6 and 37.3).
 // One CTA alone of 4 epilogue warps leaves 16 KB so that a CTA of the shrink (256 threads of 118 registers) fits
-// beside it; with more warps the registers do not, and it takes all (4096 -> 14336, 256 tokens: 67.6 -> 66.5 us; 512
+// beside it (not beside the kernel for other ranks, of 254 registers a thread); with more warps registers do not
+// allow it, and the ring takes all (4096 -> 14336, 256 tokens: 67.6 -> 66.5 us; 512
 // tokens: 126.6 -> 124.7; 128 tokens: 41.9 -> 41.5).
 StreamShape stream_shape(int T, int h, int o, int n_sms, const ClusterFit &fit, bool adapters)
 {

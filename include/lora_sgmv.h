@@ -272,7 +272,9 @@ typedef struct lora_epilogue {
  * lora_workspace_bytes(table, T).  Two launches: the tcgen05 shrink, then a persistent tcgen05
  * kernel that accumulates the base product and the adapter term in one tensor-memory tile.
  * The scaled intermediate is kept as bf16 hi + lo (16 bits of mantissa); sums are fp32; y is
- * rounded once. */
+ * rounded once.  Made for long segments: each segment costs every 256-token tile that it meets two steps of
+ * 64 columns, whatever its length and rank, where the base product takes h_in / 64 (2048 tokens, 4096 -> 14336:
+ * 168 us in 8 segments, 404 with 150 of the tokens in segments of one). */
 int lora_sgmv_layer(const lora_table *table, const lora_segments *seg, const void *x, int64_t ldx,
                     const void *W, int64_t ldw, const lora_epilogue *epilogue, void *y, int64_t ldy,
                     int32_t y_offset, void *ws, size_t ws_bytes, void *stream);
@@ -282,8 +284,10 @@ int lora_sgmv_layer(const lora_table *table, const lora_segments *seg, const voi
  * id outside [-1, n) latches LORA_STATUS_BAD_ID and leaves the token's row of y as it was.  A bf16
  * table of any rank up to LORA_MAX_RANK, without Sigma (else LORA_ERR_UNSUPPORTED); ws_bytes >=
  * lora_workspace_bytes(table, T).  Two launches: the fp32 intermediate into the workspace, then one
- * pass over W.  Without ids one launch: that pass, or in large batches the product kernel of
- * lora_sgmv_layer. */
+ * pass over W, in one of two forms by the table's ranks: a table with a rank above 64 or of no
+ * multiple of 8, or of 64 alone, takes the slower one for all of its tokens (4096 -> 14336, 64
+ * tokens of rank 16: 41.9 against 31.6 us).  Without ids one launch: that pass, or in large batches
+ * the product kernel of lora_sgmv_layer. */
 int lora_bgmv_layer(const lora_table *table, const int32_t *d_ids, int32_t T, const void *x,
                     int64_t ldx, const void *W, int64_t ldw, const lora_epilogue *epilogue, void *y,
                     int64_t ldy, int32_t y_offset, void *ws, size_t ws_bytes, void *stream);
@@ -329,7 +333,7 @@ typedef struct lora_residual {
  * fp32), the number of adapters and the status word; d need not be its h_in.  d_ids as in
  * lora_bgmv_layer: a bad id latches LORA_STATUS_BAD_ID and leaves the token's row as it was.
  * d and the row strides are multiples of 16 bytes, addresses 16-byte aligned.  h may be x (same
- * address and stride); any other overlap is LORA_ERR_INVALID_ARG.  One launch, no workspace. */
+ * address and stride); any other overlap of the two is LORA_ERR_INVALID_ARG.  One launch, no workspace. */
 int lora_norm_before(const lora_table *table, const int32_t *d_ids, int32_t T, int32_t d,
                      const void *x, int64_t ldx, const lora_norm *norm, void *h, int64_t ldh,
                      void *stream);
@@ -340,7 +344,8 @@ int lora_norm_before(const lora_table *table, const int32_t *d_ids, int32_t T, i
  * r (NULL: not wanted) and h (NULL together with next) are written once each, rounded from fp32;
  * h is computed from the unrounded r.  At least one of r and h is given.  r and h may each be z,
  * residual or a per-token gate (same address and stride), but not one another; any other overlap
- * is LORA_ERR_INVALID_ARG.  Everything else as in lora_norm_before. */
+ * with these is LORA_ERR_INVALID_ARG (weights and ids must not lie in r or h either).  Everything
+ * else as in lora_norm_before. */
 int lora_norm_after(const lora_table *table, const int32_t *d_ids, int32_t T, int32_t d,
                     const void *z, int64_t ldz, const lora_norm *norm, const lora_residual *residual,
                     void *r, int64_t ldr, const lora_norm *next, void *h, int64_t ldh, void *stream);
